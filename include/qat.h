@@ -131,7 +131,8 @@ int qat_noisy_operand(const float* W, int32_t N, int32_t K, int32_t bits, uint64
 /* Workspace sizes (bytes) for the calls below.  `raw_weights` != 0 means the
  * call is given fp32 weights to quantize itself (the workspace then also
  * holds the bf16 operands and scales); 0 means qat_qweight operands. */
-enum { QAT_OP_LINEAR_FWD = 1, QAT_OP_LINEAR_BWD = 2, QAT_OP_MLP_FWD = 3, QAT_OP_MLP_BWD = 4 };
+enum { QAT_OP_LINEAR_FWD = 1, QAT_OP_LINEAR_BWD = 2, QAT_OP_MLP_FWD = 3, QAT_OP_MLP_BWD = 4,
+       QAT_OP_CE_FWD = 5, QAT_OP_CE_BWD = 6, QAT_OP_ATTN_BWD = 7 };
 size_t qat_workspace_size(int32_t op, int32_t N_or_d, int32_t K_or_H, int64_t T,
                           int32_t raw_weights);
 
@@ -205,6 +206,45 @@ int qat_mlp_bwd(const float* Wfc, const float* Wproj, const qat_qweight* qfc,
                 int64_t T, const qat_bf16* dX_residual, qat_bf16* dX, qat_bf16* dpre_save,
                 float* dWfc, float* dWproj, int32_t accumulate_dW, void* workspace,
                 size_t ws_bytes, qat_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Softmax cross entropy of the QAT head, without keeping the logits.
+ *   logits = Z[T,d] . Wq[V,d]^T  (fp32, seen only by the GEMM's epilogue)
+ *   lse_t  = log sum_v exp(logits_tv);  loss_t = lse_t - logits_t,target
+ * The head (the tied embedding) comes as W (fp32, quantized inside the call)
+ * or qw, as in qat_linear_fwd.  V is any count up to 2^20 (a multiple of 8 is
+ * not needed), d a multiple of 8; ldz = row stride of Z in elements (0 -> d).
+ * targets [T] int64: a token whose target lies outside [0, V) (a padded row's
+ * -100, say) counts for nothing -- loss 0, gradient 0; its lse is written.
+ * loss, lse [T] fp32.  mean (nullable, 2 floats): the mean loss over the
+ * counted tokens and 1 / their number (0 and 0 when there are none).
+ * Statistics are fp32, the mean's sum fp64; the results do not depend on
+ * timing.  workspace: qat_workspace_size(QAT_OP_CE_FWD, V, d, T, raw) bytes.
+ * T = 0 writes mean only.
+ * ------------------------------------------------------------------------- */
+int qat_ce_fwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int32_t bits,
+               const qat_bf16* Z, int64_t ldz, int64_t T, const int64_t* targets, float* loss,
+               float* lse, float* mean, void* workspace, size_t ws_bytes, qat_stream_t stream);
+
+/* Gradient of qat_ce_fwd, straight through the quantizer:
+ *   g_tv = (exp(logits_tv - lse_t) - [v = target_t]) * dloss_t * gscale
+ *   dZ[T,d] = bf16( g . Wq )       (nullable)
+ *   dW[V,d] (+)= g^T . Z  in fp32  (nullable; accumulate_dW != 0 adds)
+ * lse as qat_ce_fwd wrote it; dloss [T] fp32 (nullable: 1) and gscale (one fp32
+ * on the device, nullable: 1) are the upstream gradient -- mean + 1 of
+ * qat_ce_fwd as gscale gives the gradient of the mean loss.  Tokens without a
+ * target get zero rows of dZ.  The logits are computed again and turned into g
+ * a piece of tokens at a time: g exists only for one piece, as bf16 plus the
+ * bf16 of what that rounding left (dZ takes the first, and the second at
+ * the target; dW takes both, so it is good to about 1e-5).  workspace: qat_workspace_size(QAT_OP_CE_BWD, V, d, T, raw)
+ * bytes give the pieces that run fastest and also serve qat_ce_fwd; less works
+ * with smaller pieces, down to 256 tokens (1024 bytes per word, V rounded up
+ * to a multiple of 8, and 1 KiB beside the operand), below which QAT_ERR_WORKSPACE is
+ * returned.  With T = 0, dW is zeroed unless accumulate_dW. */
+int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int32_t bits,
+               const qat_bf16* Z, int64_t ldz, int64_t T, const int64_t* targets, const float* lse,
+               const float* dloss, const float* gscale, qat_bf16* dZ, float* dW,
+               int32_t accumulate_dW, void* workspace, size_t ws_bytes, qat_stream_t stream);
 
 /* Diagnostic (the pages have no counterpart): runs the library's bounded
  * device wait on a barrier that nothing arrives on, with a limit of limit_ns

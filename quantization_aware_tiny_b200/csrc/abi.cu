@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "gemm_sm100.cuh"
+#include "lm_ops.cuh"
 #include "quant.cuh"
 
 namespace qat {
@@ -101,6 +102,37 @@ int get_operand(const float* W, const qat_qweight* qw, int64_t N, int64_t K, int
   return rc;
 }
 
+// ---- softmax cross entropy
+constexpr int64_t kCeMaxVocab = 1 << 20;
+constexpr int64_t kCeMaxTokens = (1ll << 31) - 256;
+
+// Tokens that one accumulator of dW sums.  dW of the 8,192-word head over 65,536
+// tokens is off by (relative, against 64 bits) 1.1e-5 with runs of 9,472.
+constexpr int64_t kCeTokenRun = 2048;
+
+// Row stride of the gradient pieces [rows, V]: 16-byte rows.
+inline int64_t ce_ldg(int64_t V) { return (V + 7) / 8 * 8; }
+
+// Tokens of one piece of the backward.  The product g . W has
+// ceil(rows / 256) x ceil(d / 256) tiles and reduces over the whole vocabulary
+// in each, so a piece takes as many tokens as fill the CTA pairs once (9,472 at
+// d = 512), but at most 1 GiB of gradient, and at least one row of tiles.
+int64_t ce_rows_wanted(int64_t V, int64_t d, int64_t T) {
+  const int64_t n_blk = (d + 255) / 256, pairs = sm_count() / 2;
+  int64_t rows = 256 * std::max<int64_t>(1, pairs / n_blk);
+  rows = std::min<int64_t>(rows, (1ll << 30) / (4 * ce_ldg(V)) / 256 * 256);
+  return std::min<int64_t>(std::max<int64_t>(rows, 256), T);
+}
+
+size_t ce_fwd_bytes(int64_t V, int64_t T) {
+  return align_up(ce_slots(T, V) * T * 8) + align_up(T * 4) + align_up(ce_parts_bytes(T));
+}
+size_t ce_bwd_bytes(int64_t V, int64_t rows) {
+  return 2 * align_up(rows * ce_ldg(V) * 2) + align_up(rows * 4);
+}
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
 }  // namespace
 }  // namespace qat
 
@@ -154,6 +186,13 @@ size_t qat_workspace_size(int32_t op, int32_t N_or_d, int32_t K_or_H, int64_t T,
     case QAT_OP_MLP_BWD:  // dpre [T,H] + operands
       return align_up(static_cast<size_t>(T) * b * 2) +
              (raw_weights ? operand_bytes(b, a) + operand_bytes(a, b) : 0);
+    case QAT_OP_CE_FWD:
+    case QAT_OP_CE_BWD: {  // a = V, b = d; the backward's size serves the forward too
+      if (a > kCeMaxVocab || T > kCeMaxTokens) return 0;
+      size_t n = T > 0 ? ce_fwd_bytes(a, T) : 0;
+      if (op == QAT_OP_CE_BWD && T > 0) n = std::max(n, ce_bwd_bytes(a, ce_rows_wanted(a, b, T)));
+      return n + (raw_weights ? operand_bytes(a, b) : 0);
+    }
     default:
       return 0;
   }
@@ -489,6 +528,140 @@ int dequantize_rows_batch(const qat_dequant_desc* descs, int32_t n, qat_stream_t
     b.tile_begin[i + 1] = b.tile_begin[i] + (d.items + kDequantTile - 1) / kDequantTile;
   }
   return launch_dequant_batch(b, stream);
+}
+
+int qat_ce_fwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int32_t bits,
+               const qat_bf16* Z, int64_t ldz, int64_t T, const int64_t* targets, float* loss,
+               float* lse, float* mean, void* workspace, size_t ws_bytes, qat_stream_t stream) {
+  if (T < 0 || V <= 0 || !bits_ok(bits) || (T > 0 && (!Z || !targets || !loss || !lse)))
+    return QAT_ERR_ARG;
+  if ((W == nullptr) == (qw == nullptr)) return QAT_ERR_ARG;
+  if (!dim_ok(d) || V > kCeMaxVocab || T > kCeMaxTokens) return QAT_ERR_SHAPE;
+  if (ldz == 0) ldz = d;
+  if (ldz < d || (ldz & 7)) return QAT_ERR_SHAPE;
+  if (!aligned_to(targets, 8) || !aligned_to(loss, 4) || !aligned_to(lse, 4) || !aligned_to(mean, 4))
+    return QAT_ERR_ALIGN;
+  if (T == 0)
+    return mean ? cuda_status(cudaMemsetAsync(mean, 0, 8, stream)) : static_cast<int>(QAT_OK);
+  if (!aligned16(Z) || !aligned16(workspace)) return QAT_ERR_ALIGN;
+  Carver ws(workspace, ws_bytes);
+  CeJoin j{};
+  j.slots = static_cast<int>(ce_slots(T, V));
+  float2* stats = static_cast<float2*>(ws.take(static_cast<size_t>(j.slots) * T * 8));
+  float* tlogit = static_cast<float*>(ws.take(static_cast<size_t>(T) * 4));
+  j.parts = ws.take(ce_parts_bytes(T));
+  if (!stats || !tlogit || !j.parts) return QAT_ERR_WORKSPACE;
+  const __nv_bfloat16* op = nullptr;
+  int rc = get_operand(W, qw, V, d, bits, ws, stream, &op);
+  if (rc) return rc;
+  GemmDesc g;  // logits = Z . Wq^T, as tiles that only the epilogue sees
+  g.A = Z; g.lda = ldz;
+  g.B = op; g.ldb = d;
+  g.M = T; g.N = V; g.K = d;
+  g.epi = EPI_CE_STATS;
+  g.ce.targets = targets;
+  g.ce.vocab = V;
+  g.ce.stats = stats;
+  g.ce.tlogit = tlogit;
+  rc = launch_gemm(g, stream);
+  if (rc) return rc;
+  j.stats = stats;
+  j.tlogit = tlogit;
+  j.targets = targets;
+  j.loss = loss;
+  j.lse = lse;
+  j.mean = mean;
+  j.T = T;
+  j.vocab = V;
+  return launch_ce_join(j, stream);
+}
+
+int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int32_t bits,
+               const qat_bf16* Z, int64_t ldz, int64_t T, const int64_t* targets, const float* lse,
+               const float* dloss, const float* gscale, qat_bf16* dZ, float* dW,
+               int32_t accumulate_dW, void* workspace, size_t ws_bytes, qat_stream_t stream) {
+  if (T < 0 || V <= 0 || !bits_ok(bits) || (T > 0 && (!Z || !targets || !lse))) return QAT_ERR_ARG;
+  if ((W == nullptr) == (qw == nullptr)) return QAT_ERR_ARG;
+  if (!dim_ok(d) || V > kCeMaxVocab || T > kCeMaxTokens) return QAT_ERR_SHAPE;
+  if (ldz == 0) ldz = d;
+  if (ldz < d || (ldz & 7)) return QAT_ERR_SHAPE;
+  if (!aligned_to(targets, 8) || !aligned_to(lse, 4) || !aligned_to(dloss, 4) ||
+      !aligned_to(gscale, 4))
+    return QAT_ERR_ALIGN;
+  if ((dZ && !aligned16(dZ)) || (dW && !aligned16(dW))) return QAT_ERR_ALIGN;
+  if (!dZ && !dW) return QAT_OK;
+  if (T == 0) {
+    if (dW && !accumulate_dW)
+      return cuda_status(cudaMemsetAsync(dW, 0, static_cast<size_t>(V) * d * 4, stream));
+    return QAT_OK;
+  }
+  if (!aligned16(Z) || !aligned16(workspace)) return QAT_ERR_ALIGN;
+  Carver ws(workspace, ws_bytes);
+  const __nv_bfloat16* op = nullptr;
+  int rc = get_operand(W, qw, V, d, bits, ws, stream, &op);
+  if (rc) return rc;
+  // Tokens of a piece: what the operator asks for, or what the workspace holds
+  // (whole row tiles), down to one of them.
+  const int64_t ldg = ce_ldg(V);
+  int64_t rows = ce_rows_wanted(V, d, T);
+  const size_t left = ws_bytes > ws.used ? ws_bytes - ws.used : 0;
+  if (ce_bwd_bytes(V, rows) > left) {
+    rows = static_cast<int64_t>(left / (4 * static_cast<size_t>(ldg))) / 256 * 256;
+    while (rows > 0 && ce_bwd_bytes(V, rows) > left) rows -= 256;
+    if (rows <= 0) return QAT_ERR_WORKSPACE;
+  }
+  void* ghi = ws.take(static_cast<size_t>(rows) * ldg * 2);
+  void* glo = ws.take(static_cast<size_t>(rows) * ldg * 2);
+  float* rem = static_cast<float*>(ws.take(static_cast<size_t>(rows) * 4));
+  if (!ghi || !glo || !rem) return QAT_ERR_WORKSPACE;
+  for (int64_t t0 = 0; t0 < T; t0 += rows) {
+    const int64_t n = std::min(rows, T - t0);
+    const qat_bf16* Zp = Z + t0 * ldz;
+    GemmDesc g;  // g = (softmax(Z . Wq^T) - [target]) * dloss, as bf16 and its remainder
+    g.A = Zp; g.lda = ldz;
+    g.B = op; g.ldb = d;
+    g.M = n; g.N = V; g.K = d;
+    g.epi = EPI_CE_GRAD;
+    g.D = ghi; g.ldd = ldg;
+    g.D2 = dW ? glo : nullptr; g.ldd2 = ldg;
+    g.ce.targets = targets + t0;
+    g.ce.vocab = V;
+    g.ce.rem = dZ ? rem : nullptr;
+    g.ce.lse = lse + t0;
+    g.ce.dloss = dloss ? dloss + t0 : nullptr;
+    g.ce.gscale = gscale;
+    rc = launch_gemm(g, stream);
+    if (rc) return rc;
+    if (dZ) {  // dZ = g . Wq from g's bf16 half, the target's remainder added at the end
+      GemmDesc x;
+      x.A = ghi; x.lda = ldg;
+      x.B = op; x.ldb = d; x.b_mn = true;
+      x.M = n; x.N = d; x.K = V;
+      x.epi = EPI_CE_DZ;
+      x.D = dZ + t0 * d; x.ldd = d;
+      x.ce.targets = targets + t0;
+      x.ce.vocab = V;
+      x.ce.rem = rem;
+      x.ce.words = op;
+      rc = launch_gemm(x, stream);
+      if (rc) return rc;
+    }
+    // dW (+)= g^T . Z, kept in 32 bits: g's bf16 rounding alone would leave it
+    // 1e-3 off, so its remainder is multiplied too (and first: it is small).
+    for (int half = 0; dW && half < 2; ++half) {
+      GemmDesc w;
+      w.A = half ? ghi : glo; w.lda = ldg; w.a_mn = true;
+      w.B = Zp; w.ldb = ldz; w.b_mn = true;
+      w.M = V; w.N = d; w.K = n;
+      w.epi = EPI_F32;
+      w.D = dW; w.ldd = d;
+      w.k_run = kCeTokenRun;
+      w.accumulate = accumulate_dW != 0 || t0 > 0 || half > 0;
+      rc = launch_gemm(w, stream);
+      if (rc) return rc;
+    }
+  }
+  return QAT_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,129 @@
+// Reductions of the softmax cross entropy.  The logits themselves only ever
+// exist as accumulator tiles of the GEMM (its EPI_CE_STATS and EPI_CE_GRAD
+// epilogues); what reaches global memory is one (max, sum) pair per token and
+// 128 columns, joined here.
+#include <algorithm>
+
+#include "lm_ops.cuh"
+
+namespace qat {
+
+namespace {
+
+constexpr int kJoinRows = 32;   // tokens of a block: one per lane, so the pairs load coalesced
+constexpr int kJoinWarps = 8;   // slots are dealt to the warps in turn
+
+// (sum of losses, counted tokens) of a block of kJoinRows tokens.
+struct alignas(16) CePart {
+  double sum;
+  int64_t count;
+};
+
+// (m, s) <- the statistics of both halves: s = sum of exp(l - m) over both.
+// m = -inf marks an empty half (s = 0).
+__device__ __forceinline__ void merge_stats(float& m, float& s, float m2, float s2) {
+  const float t = fmaxf(m, m2);
+  if (t == -INFINITY) return;
+  s = s * expf(m - t) + s2 * expf(m2 - t);
+  m = t;
+}
+
+// lse = m + log s, loss = lse - logit of the target (0 without one).  Bound by
+// reading slots * T pairs: 33.5 MB for 65,536 tokens of 8,192 words.
+__global__ void __launch_bounds__(kJoinRows* kJoinWarps) ce_join_kernel(const CeJoin j) {
+  __shared__ float2 part[kJoinWarps][kJoinRows];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kJoinRows + lane;
+  float m = -INFINITY, s = 0.0f;
+  if (t < j.T) {
+#pragma unroll 4
+    for (int i = w; i < j.slots; i += kJoinWarps) {
+      const float2 v = j.stats[static_cast<int64_t>(i) * j.T + t];
+      merge_stats(m, s, v.x, v.y);
+    }
+  }
+  part[w][lane] = make_float2(m, s);
+  __syncthreads();
+  if (w != 0) return;
+#pragma unroll
+  for (int i = 1; i < kJoinWarps; ++i) merge_stats(m, s, part[i][lane].x, part[i][lane].y);
+  double sum = 0.0;
+  int count = 0;
+  if (t < j.T) {
+    const float lse = m + logf(s);
+    const int64_t y = j.targets[t];
+    float loss = 0.0f;
+    if (y >= 0 && y < j.vocab) {
+      loss = lse - j.tlogit[t];
+      sum = loss;
+      count = 1;
+    }
+    j.lse[t] = lse;
+    j.loss[t] = loss;
+  }
+  if (!j.mean) return;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    count += __shfl_xor_sync(0xffffffffu, count, o);
+  }
+  if (lane == 0) static_cast<CePart*>(j.parts)[blockIdx.x] = CePart{sum, count};
+}
+
+// Mean loss over the counted tokens: the blocks' sums in 64 bits and in a fixed
+// order, so the same inputs always give the same bits.
+__global__ void __launch_bounds__(1024) ce_mean_kernel(const CePart* parts, int64_t n, float* mean) {
+  __shared__ double ssum[32];
+  __shared__ int64_t scnt[32];
+  double sum = 0.0;
+  int64_t count = 0;
+  for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
+    sum += parts[i].sum;
+    count += parts[i].count;
+  }
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    count += __shfl_xor_sync(0xffffffffu, count, o);
+  }
+  if (lane == 0) {
+    ssum[w] = sum;
+    scnt[w] = count;
+  }
+  __syncthreads();
+  if (w != 0) return;
+  const int warps = blockDim.x >> 5;
+  sum = lane < warps ? ssum[lane] : 0.0;
+  count = lane < warps ? scnt[lane] : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    count += __shfl_xor_sync(0xffffffffu, count, o);
+  }
+  if (lane == 0) {
+    mean[0] = count ? static_cast<float>(sum / static_cast<double>(count)) : 0.0f;
+    mean[1] = count ? static_cast<float>(1.0 / static_cast<double>(count)) : 0.0f;
+  }
+}
+
+int64_t join_blocks(int64_t T) { return (T + kJoinRows - 1) / kJoinRows; }
+
+}  // namespace
+
+int64_t ce_parts_bytes(int64_t T) { return join_blocks(T) * static_cast<int64_t>(sizeof(CePart)); }
+
+int launch_ce_join(const CeJoin& j, cudaStream_t stream) {
+  const int64_t blocks = join_blocks(j.T);
+  ce_join_kernel<<<static_cast<unsigned>(blocks), kJoinRows * kJoinWarps, 0, stream>>>(j);
+  count_launch();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return QAT_ERR_CUDA;
+  if (!j.mean) return QAT_OK;
+  const int threads = static_cast<int>(std::min<int64_t>(1024, (blocks + 31) / 32 * 32));
+  ce_mean_kernel<<<1, threads, 0, stream>>>(static_cast<const CePart*>(j.parts), blocks, j.mean);
+  count_launch();
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace qat

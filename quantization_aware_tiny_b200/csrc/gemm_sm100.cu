@@ -44,7 +44,7 @@ template <int BN, bool PAIR, int EPI, bool FB = false>
 struct Cfg {
   static constexpr bool F32 = (EPI == EPI_F32 || EPI == EPI_F32_ATOMIC);
   static constexpr bool HAS_R = epi_reads_r(EPI);
-  static constexpr bool ACT = epi_act_fwd(EPI);
+  static constexpr bool ACT = epi_act_fwd(EPI) || EPI == EPI_CE_GRAD;  // two bf16 outputs
   static constexpr int EW = F32 ? 4 : (FB && (ACT || HAS_R)) ? 4 : 8;  // epilogue warps
   static constexpr int THREADS = 64 + 32 * EW;
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // B rows staged by one CTA
@@ -80,6 +80,7 @@ struct Cfg {
 struct KArgs {
   int M, N;
   int num_m_blk, num_n_blk, splits, kblk_total, kblk_per_split, num_tiles;
+  int ordered;  // EPI_F32_ATOMIC: one CTA (pair) takes all splits of a tile, in order
   void* D;
   int64_t ldd;
   void* D2;
@@ -91,9 +92,81 @@ struct KArgs {
   const float* W;  // FB: fp32 weight [N, K] row-major, quantized in the producer
   int K;           // FB: reduction length
   int bits;        // FB: grid (5, 6 or 8)
+  CeArgs ce;       // cross-entropy epilogues
 };
 
 __device__ __forceinline__ float bf2f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x to about 2^-22 relative (the special-function unit; 0 for x = -inf).
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// What the cross-entropy epilogues keep of this lane's row of a tile.
+//   STATS: m, s = running max and sum of exp(logit - m) over the columns seen
+//   GRAD:  lse2 = lse * log2(e), scale = the row's upstream gradient (0: no target)
+struct CeRow {
+  int target;  // column of the target, -1: none
+  float m, s, lse2, scale;
+};
+
+// Softmax statistics of one 32-column chunk of this lane's row: one pass, the
+// sum rescaled whenever the running maximum moves.  The target's logit is
+// picked out only in chunks that hold some lane's target (a warp vote), so the
+// 32 compares are paid in few of them.
+__device__ __forceinline__ void ce_stats_chunk(const KArgs& p, uint32_t (&acc)[32], int col0,
+                                               int row, CeRow& c) {
+  float* v = reinterpret_cast<float*>(acc);
+  if (col0 + 32 > p.N) {  // columns behind the vocabulary
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (col0 + j >= p.N) v[j] = -INFINITY;
+  }
+  const int idx = c.target - col0;
+  const bool here = c.target >= 0 && idx >= 0 && idx < 32;
+  if (__any_sync(0xffffffffu, here)) {
+    float t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) t = (j == idx) ? v[j] : t;
+    if (here) p.ce.tlogit[row] = t;
+  }
+  float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int j = 4; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+  const float m = fmaxf(c.m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+  const float m2 = m * kLog2e;
+  float sum[4] = {c.s * exp2_fast(fmaf(c.m, kLog2e, -m2)), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) sum[j & 3] += exp2_fast(fmaf(v[j], kLog2e, -m2));
+  c.m = m;
+  c.s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+// Gradient of one 32-column chunk in place: acc <- (softmax - [target]) * scale.
+__device__ __forceinline__ void ce_grad_chunk(const KArgs& p, uint32_t (&acc)[32], int col0,
+                                              int row, const CeRow& c) {
+  float* v = reinterpret_cast<float*>(acc);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = exp2_fast(fmaf(v[j], kLog2e, -c.lse2));
+  const int idx = c.target - col0;
+  const bool here = c.target >= 0 && idx >= 0 && idx < 32;
+  if (__any_sync(0xffffffffu, here)) {
+    float t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      v[j] -= (here && j == idx) ? 1.0f : 0.0f;
+      t = (j == idx) ? v[j] : t;
+    }
+    t *= c.scale;
+    if (here && p.ce.rem) p.ce.rem[row] = t - bf2f(__float2bfloat16_rn(t));
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] *= c.scale;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 v = __floats2bfloat162_rn(a, b);  // .x = a (low half), .y = b
@@ -109,7 +182,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 template <int EPI>
 __device__ __forceinline__ void stage_chunk(const KArgs& p, const uint32_t (&acc)[32],
                                             const uint4 (&rin)[4], uint32_t buf0, uint32_t buf1,
-                                            int lane) {
+                                            int lane, float rem) {
   const float* v = reinterpret_cast<const float*>(acc);
   if constexpr (EPI == EPI_F32 || EPI == EPI_F32_ATOMIC) {
     const uint32_t row = buf0 + static_cast<uint32_t>(lane) * 128u;
@@ -129,6 +202,8 @@ __device__ __forceinline__ void stage_chunk(const KArgs& p, const uint32_t (&acc
         const float a = v[8 * j + i];
         if constexpr (EPI == EPI_BF16) {
           o[i] = a;
+        } else if constexpr (EPI == EPI_CE_DZ) {
+          o[i] = fmaf(rem, bf2f(r[i]), a);
         } else if constexpr (EPI == EPI_BF16_RESID) {
           o[i] = __fadd_rn(a, bf2f(r[i]));
         } else if constexpr (EPI == EPI_DRELU2) {
@@ -137,6 +212,8 @@ __device__ __forceinline__ void stage_chunk(const KArgs& p, const uint32_t (&acc
           // d/dx leaky(x, 0.5)^2 = 2x (x > 0), x/2 (x <= 0): the scalings are exact
           const float pre = bf2f(r[i]);
           o[i] = __fmul_rn(a, pre > 0.0f ? __fmul_rn(pre, 2.0f) : __fmul_rn(pre, 0.5f));
+        } else if constexpr (EPI == EPI_CE_GRAD) {  // buf0 <- bf16(g), buf1 <- bf16(g - bf16(g))
+          o[i] = __fsub_rn(a, bf2f(__float2bfloat16_rn(a)));
         } else if constexpr (EPI == EPI_LRELU2) {  // buf1 <- leaky_relu(acc, 0.5)^2
           const float t = a > 0.0f ? a : __fmul_rn(a, 0.5f);
           o[i] = __fmul_rn(t, t);
@@ -146,7 +223,7 @@ __device__ __forceinline__ void stage_chunk(const KArgs& p, const uint32_t (&acc
         }
       }
       const uint32_t at = off + (static_cast<uint32_t>(j ^ sw) << 4);
-      if constexpr (epi_act_fwd(EPI)) {
+      if constexpr (epi_act_fwd(EPI) || EPI == EPI_CE_GRAD) {
         st_shared_v4(buf0 + at, pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
                      pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
         st_shared_v4(buf1 + at, pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
@@ -289,16 +366,32 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
     const int64_t s = q * p.num_tiles / units;
     return s < x + p.num_m_blk ? static_cast<int>(s - x) : 0;
   };
-  auto tile_nb = [&](int t) { return FB ? t / p.num_m_blk : t % p.num_n_blk; };
+  // Ordered splits: tile numbers run split-fastest and a CTA (pair) walks all
+  // splits of a tile before its next tile, so every element's partial sums are
+  // added in the same order each time.
+  const bool ordered = EPI == EPI_F32_ATOMIC && p.ordered != 0;
+  if (ordered) t_begin = unit * p.splits;
+  auto next_tile = [&](int t) {
+    if (ordered) return (t + 1) % p.splits ? t + 1 : t + 1 + (units - 1) * p.splits;
+    return t + t_step;
+  };
+  auto tile_nb = [&](int t) {
+    if (ordered) return t / p.splits % p.num_n_blk;
+    return FB ? t / p.num_m_blk : t % p.num_n_blk;
+  };
   auto tile_mb = [&](int t) {
     if constexpr (FB) {
       const int nb = t / p.num_m_blk;
       const int r = t - nb * p.num_m_blk - fb_base(nb);
       return r < 0 ? r + p.num_m_blk : r;
     }
+    if (ordered) return t / p.splits / p.num_n_blk;
     return (t / p.num_n_blk) % p.num_m_blk;
   };
-  auto tile_sp = [&](int t) { return FB ? 0 : t / (p.num_n_blk * p.num_m_blk); };
+  auto tile_sp = [&](int t) {
+    if (ordered) return t % p.splits;
+    return FB ? 0 : t / (p.num_n_blk * p.num_m_blk);
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -347,7 +440,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
       int stage = 0, pos = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = t_begin; ok && tile < t_end; tile += t_step) {
+      for (int tile = t_begin; ok && tile < t_end; tile = next_tile(tile)) {
         const int nb = tile_nb(tile);
         const int mb = tile_mb(tile);
         const int sp = tile_sp(tile);
@@ -423,7 +516,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
       };
       int panel_nb = -1;  // FB: N block whose panel the MMAs read
       uint32_t panel_phase = 0;
-      for (int tile = t_begin; ok && tile < t_end; tile += t_step) {
+      for (int tile = t_begin; ok && tile < t_end; tile = next_tile(tile)) {
         const int sp = tile_sp(tile);
         const int kb0 = sp * p.kblk_per_split;
         const int kb1 = min(kb0 + p.kblk_per_split, p.kblk_total);
@@ -480,6 +573,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
     uint8_t* rbuf = rstage + ew * C::R_BUFS * 2048;
     uint64_t* rb = rbar + ew * C::R_BUFS;
     const bool keep_pre = epi_act_fwd(EPI) && p.D != nullptr;
+    const bool keep_lo = EPI == EPI_CE_GRAD && p.D2 != nullptr;
     int acc = 0;
     uint32_t acc_phase = 0;
     uint32_t chunk = 0;
@@ -525,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
       }
       if (t_begin < t_end) produce_panel(tile_nb(t_begin));
     }
-    for (int tile = t_begin; tile < t_end; tile += t_step) {
+    for (int tile = t_begin; tile < t_end; tile = next_tile(tile)) {
       const int nb = tile_nb(tile);
       const int mb = tile_mb(tile);
       if constexpr (FB) {
@@ -551,6 +645,22 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
       };
       if constexpr (kR) {
         for (int i = 0; i < mine && i < C::R_BUFS; ++i) issue_r(i);
+      }
+      CeRow ce;
+      const int ce_row = row0 + lane;
+      if constexpr (epi_ce(EPI)) {  // this lane's row, before the accumulator is waited for
+        const bool valid = ce_row < p.M;
+        const int64_t t = valid ? p.ce.targets[ce_row] : -1;
+        ce.target = (t >= 0 && t < p.ce.vocab) ? static_cast<int>(t) : -1;
+        ce.m = -INFINITY;
+        ce.s = 0.0f;
+        if constexpr (EPI == EPI_CE_DZ) ce.scale = ce.target >= 0 ? p.ce.rem[ce_row] : 0.0f;
+        if constexpr (EPI == EPI_CE_GRAD) {
+          ce.lse2 = valid ? p.ce.lse[ce_row] * kLog2e : 0.0f;
+          ce.scale = 0.0f;
+          if (ce.target >= 0)
+            ce.scale = (p.ce.dloss ? p.ce.dloss[ce_row] : 1.0f) * (p.ce.gscale ? *p.ce.gscale : 1.0f);
+        }
       }
       if (!mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err)) break;
       tc_fence_after();
@@ -589,16 +699,29 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
           __syncwarp();
           if (i + C::R_BUFS < mine) issue_r(i + C::R_BUFS);
         }
+        if constexpr (EPI == EPI_CE_DZ) {  // the target's row of the operand (N is a multiple of 8)
+          if (ce.target >= 0) {
+            const __nv_bfloat16* w = p.ce.words + static_cast<int64_t>(ce.target) * p.N + col0;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (col0 + 8 * g < p.N) rin[g] = __ldg(reinterpret_cast<const uint4*>(w) + g);
+          }
+        }
         uint32_t r[32];
         tmem_ld32(t_row + static_cast<uint32_t>(c * 32), r);
         tmem_ld_wait();
         if (i == mine - 1) release_acc();  // hand the accumulator back to the MMA
+        if constexpr (EPI == EPI_CE_STATS) {
+          ce_stats_chunk(p, r, col0, ce_row, ce);
+          continue;
+        }
+        if constexpr (EPI == EPI_CE_GRAD) ce_grad_chunk(p, r, col0, ce_row, ce);
         const uint32_t b = chunk & 1u;
         const uint32_t buf0 = kF32 ? wbuf + b * 4096u : wbuf + b * 2048u;
         const uint32_t buf1 = wbuf + 4096u + b * 2048u;
         if (lane == 0) bulk_wait_read<1>();  // the store that last used buffer b is done reading
         __syncwarp();
-        stage_chunk<EPI>(p, r, rin, buf0, buf1, lane);
+        stage_chunk<EPI>(p, r, rin, buf0, buf1, lane, EPI == EPI_CE_DZ ? ce.scale : 0.0f);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -608,6 +731,9 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
           } else if constexpr (epi_act_fwd(EPI)) {
             if (keep_pre) tma_store_2d(&tmD, s0, col0, row0);
             tma_store_2d(&tmD2, staging + (buf1 - smem_u32(staging)), col0, row0);
+          } else if constexpr (EPI == EPI_CE_GRAD) {
+            tma_store_2d(&tmD, s0, col0, row0);
+            if (keep_lo) tma_store_2d(&tmD2, staging + (buf1 - smem_u32(staging)), col0, row0);
           } else {
             tma_store_2d(&tmD, s0, col0, row0);
           }
@@ -615,6 +741,12 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
         }
       }
       if (!ok) break;
+      // the next split of this tile adds to the same elements: let these adds land first
+      if (ordered && lane == 0) bulk_wait_all();
+      if constexpr (EPI == EPI_CE_STATS) {  // this warp's share of the row's N block (none: m = -inf)
+        if (ce_row < p.M)
+          p.ce.stats[static_cast<int64_t>(nb * kSplit + h) * p.M + ce_row] = make_float2(ce.m, ce.s);
+      }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -753,6 +885,10 @@ int dispatch_bn(const GemmDesc& g, const CUtensorMap& ma, const CUtensorMap& mb,
       case EPI_RELU2: return launch_t<BN, false, false, EPI_RELU2, PAIR>(ma, mb, md, md2, mr, a, s);
       case EPI_LRELU2:
         return launch_t<BN, false, false, EPI_LRELU2, PAIR>(ma, mb, md, md2, mr, a, s);
+      case EPI_CE_STATS:
+        return launch_t<BN, false, false, EPI_CE_STATS, PAIR>(ma, mb, md, md2, mr, a, s);
+      case EPI_CE_GRAD:
+        return launch_t<BN, false, false, EPI_CE_GRAD, PAIR>(ma, mb, md, md2, mr, a, s);
       default: break;
     }
   } else if (!g.a_mn && g.b_mn) {
@@ -763,6 +899,7 @@ int dispatch_bn(const GemmDesc& g, const CUtensorMap& ma, const CUtensorMap& mb,
       case EPI_DRELU2: return launch_t<BN, false, true, EPI_DRELU2, PAIR>(ma, mb, md, md2, mr, a, s);
       case EPI_DLRELU2:
         return launch_t<BN, false, true, EPI_DLRELU2, PAIR>(ma, mb, md, md2, mr, a, s);
+      case EPI_CE_DZ: return launch_t<BN, false, true, EPI_CE_DZ, PAIR>(ma, mb, md, md2, mr, a, s);
       default: break;
     }
   } else if (g.a_mn && g.b_mn) {
@@ -828,7 +965,42 @@ int choose_splits(int tiles, int kblk, int sms) {
   return best_s;
 }
 
+// N tile.  GEMMs with at least 256 rows run on CTA pairs 256 columns wide,
+// the last N block partial where 256 does not divide N: the forward and dX
+// GEMMs (bf16 output) when N >= 160, and the weight-gradient GEMMs (both
+// operands MN-major).  The rest take 256 (paired when M >= 256) unless 128
+// wastes fewer columns.  (For the d = 640 core's backward, 256-wide pairs
+// against 128-wide single-CTA tiles: dX GEMMs 57 -> 44 us (N = 640,
+// K = 1920) and 58 -> 50 us (N = 1920, K = 640), weight gradients 33 -> 25 us
+// (640 x 640) and 70 -> 64 us (1920 x 640), per 16,384 tokens.)
+// 256 wide even when it does not divide N (the last N block is partial):
+// narrower tiles re-read A once more per FLOP, and with K this short the
+// operand stream from L2 then sets the pace (d = 640 core: 160-wide tiles
+// for N = 640, 192-wide for N = 1920 took 0.417 ms per R = 3 forward,
+// 256-wide everywhere 0.365 ms; a wave-count rule -- the width of fewest
+// ceil(tiles / pairs) * BN -- was slower too, 0.42 -> 0.44 ms).
+void choose_tile(int64_t M, int64_t N, bool fp32_out, bool a_mn, int* BN, bool* pair) {
+  if (M >= 256 && N >= 160 && (a_mn || !fp32_out)) {
+    *pair = true;
+    *BN = 256;
+    return;
+  }
+  const int64_t pad256 = (N + 255) / 256 * 256 - N;
+  const int64_t pad128 = (N + 127) / 128 * 128 - N;
+  *BN = (pad128 < pad256) ? 128 : 256;
+  *pair = (*BN == 256) && M >= 256;
+}
+
 }  // namespace
+
+int64_t ce_slots(int64_t M, int64_t N) {
+  int BN;
+  bool pair;
+  choose_tile(M, N, false, false, &BN, &pair);
+  static_assert(Cfg<256, true, EPI_CE_STATS>::EW == 8 && Cfg<128, false, EPI_CE_STATS>::EW == 8,
+                "two epilogue warps share a lane quarter");
+  return (N + BN - 1) / BN * 2;
+}
 
 bool fused_b_supported(int64_t M, int64_t N, int64_t K, int epi) {
   const bool fwd_epi = epi == EPI_BF16 || epi == EPI_BF16_RESID || epi == EPI_RELU2 || epi == EPI_LRELU2;
@@ -838,7 +1010,15 @@ bool fused_b_supported(int64_t M, int64_t N, int64_t K, int epi) {
 int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
   if (g.M < 0 || g.N <= 0 || g.K <= 0) return QAT_ERR_ARG;
   if (g.M == 0) return QAT_OK;
-  if (!g.A || (!g.B && !g.Wraw) || (!g.D && !epi_act_fwd(g.epi))) return QAT_ERR_ARG;
+  if (!g.A || (!g.B && !g.Wraw) || (!g.D && !epi_act_fwd(g.epi) && g.epi != EPI_CE_STATS))
+    return QAT_ERR_ARG;
+  if (epi_ce(g.epi)) {
+    const CeArgs& c = g.ce;
+    if (!c.targets || c.vocab <= 0) return QAT_ERR_ARG;
+    if (g.epi == EPI_CE_STATS && (!c.stats || !c.tlogit || c.vocab != g.N)) return QAT_ERR_ARG;
+    if (g.epi == EPI_CE_GRAD && (!c.lse || c.vocab != g.N)) return QAT_ERR_ARG;
+    if (g.epi == EPI_CE_DZ && (!c.rem || !c.words || !aligned16(c.words))) return QAT_ERR_ARG;
+  }
   if (g.Wraw && (!fused_b_supported(g.M, g.N, g.K, g.epi) || g.a_mn || g.b_mn))
     return QAT_ERR_UNSUPPORTED;
   if (g.Wraw && (!aligned16(g.Wraw) || (g.bits != 5 && g.bits != 6 && g.bits != 8)))
@@ -848,42 +1028,19 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
   if (!aligned16(g.A) || (g.B && !aligned16(g.B)) || (g.D && !aligned16(g.D)) || (g.D2 && !aligned16(g.D2)) ||
       (g.R && !aligned16(g.R)))
     return QAT_ERR_ALIGN;
-  if ((g.N & 7) || (g.lda & 7) || (g.ldb & 7) || (g.ldd & 7) || (g.D2 && (g.ldd2 & 7)) ||
+  // (the logits' epilogues take any N: their outputs are clipped to N columns of rows ldd apart)
+  if (((g.N & 7) && g.epi != EPI_CE_STATS && g.epi != EPI_CE_GRAD) || (g.lda & 7) || (g.ldb & 7) || (g.ldd & 7) || (g.D2 && (g.ldd2 & 7)) ||
       (g.R && (g.ldr & 7)))
     return QAT_ERR_SHAPE;
   if (g.M > (1ll << 31) - 256 || g.N > (1 << 30) || g.K > (1ll << 31) - 256) return QAT_ERR_SHAPE;
 
-  // N tile.  GEMMs with at least 256 rows run on CTA pairs 256 columns wide,
-  // the last N block partial where 256 does not divide N: the forward and dX
-  // GEMMs (bf16 output) when N >= 160, and the weight-gradient GEMMs (both
-  // operands MN-major).  The rest take 256 (paired when M >= 256) unless 128
-  // wastes fewer columns.  (For the d = 640 core's backward, 256-wide pairs
-  // against 128-wide single-CTA tiles: dX GEMMs 57 -> 44 us (N = 640,
-  // K = 1920) and 58 -> 50 us (N = 1920, K = 640), weight gradients 33 -> 25 us
-  // (640 x 640) and 70 -> 64 us (1920 x 640), per 16,384 tokens.)
   int BN;
   bool pair;
-  const bool kmajor_fwd = (!g.a_mn && g.epi != EPI_F32 && g.epi != EPI_F32_ATOMIC) ||
-                          (g.a_mn && g.M >= 256);
   if (g.Wraw) {
     pair = true;
     BN = fused_b_bn(g.N, g.K);
-  } else if (kmajor_fwd && g.M >= 256 && g.N >= 160) {
-    pair = true;
-    // (a wave-count rule -- the width of fewest ceil(tiles / pairs) * BN -- was
-    // slower: 160-wide tiles for the d = 640 core's N = 1280 filled the waves
-    // better but cost more operand traffic per FLOP, core 0.42 -> 0.44 ms)
-    // 256 wide even when it does not divide N (the last N block is partial):
-    // narrower tiles re-read A once more per FLOP, and with K this short the
-    // operand stream from L2 then sets the pace (d = 640 core: 160-wide tiles
-    // for N = 640, 192-wide for N = 1920 took 0.417 ms per R = 3 forward,
-    // 256-wide everywhere 0.365 ms)
-    BN = 256;
   } else {
-    const int64_t pad256 = (g.N + 255) / 256 * 256 - g.N;
-    const int64_t pad128 = (g.N + 127) / 128 * 128 - g.N;
-    BN = (pad128 < pad256) ? 128 : 256;
-    pair = (BN == 256) && g.M >= 256;
+    choose_tile(g.M, g.N, g.epi == EPI_F32 || g.epi == EPI_F32_ATOMIC, g.a_mn, &BN, &pair);
   }
   const int tile_m = pair ? 2 * BM : BM;
 
@@ -905,6 +1062,7 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
   a.W = g.Wraw;
   a.K = static_cast<int>(g.K);
   a.bits = g.bits;
+  a.ce = g.ce;
 
   int epi = g.epi;
   if (epi == EPI_F32 || epi == EPI_F32_ATOMIC) {
@@ -916,6 +1074,11 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
     // tokens: 64 tiles on 74 pairs, 447-461 us split 8 ways, 424-426 us whole).
     const int cunits = pair ? sm_count() / 2 : sm_count();
     int s = (2 * tiles >= cunits) ? 1 : choose_splits(tiles, a.kblk_total, cunits);
+    const int run = static_cast<int>(g.k_run / BK);
+    if (run > 0 && (a.kblk_total + s - 1) / s > run) {
+      a.ordered = s == 1;
+      s = (a.kblk_total + run - 1) / run;
+    }
     a.kblk_per_split = (a.kblk_total + s - 1) / s;
     s = (a.kblk_total + a.kblk_per_split - 1) / a.kblk_per_split;  // no empty split
     a.splits = s;
@@ -952,14 +1115,16 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
     if (rc) return rc;
   }
   // Output maps: 32x32 boxes, bf16 with 64-byte swizzle or fp32 with 128-byte swizzle.
-  CUtensorMap md, md2;
+  CUtensorMap md = ma, md2 = ma;
   const bool f32 = (epi == EPI_F32 || epi == EPI_F32_ATOMIC);
   const void* d_base = g.D ? g.D : g.D2;
   const int64_t d_ld = g.D ? g.ldd : g.ldd2;
-  rc = make_out_map(&md, d_base, g.N, g.M, d_ld, f32);
-  if (rc) return rc;
-  rc = make_out_map(&md2, g.D2 ? g.D2 : d_base, g.N, g.M, g.D2 ? g.ldd2 : d_ld, false);
-  if (rc) return rc;
+  if (g.epi != EPI_CE_STATS) {  // (the statistics have no tiled output)
+    rc = make_out_map(&md, d_base, g.N, g.M, d_ld, f32);
+    if (rc) return rc;
+    rc = make_out_map(&md2, g.D2 ? g.D2 : d_base, g.N, g.M, g.D2 ? g.ldd2 : d_ld, false);
+    if (rc) return rc;
+  }
   CUtensorMap mr = md;
   if (epi_reads_r(g.epi)) {
     rc = make_out_map(&mr, g.R, g.N, g.M, g.ldr, false);

@@ -15,6 +15,9 @@ enum Epi : int {
   EPI_F32_ATOMIC = 5,  // D += acc with atomics (split-K partial sums)
   EPI_LRELU2 = 6,      // D = bf16(acc) (optional), D2 = bf16(leaky_relu(acc, 0.5)^2)
   EPI_DLRELU2 = 7,     // D = bf16(acc * g(R)), g = 2R for R > 0 else R/2 (its derivative)
+  EPI_CE_STATS = 8,    // no D: per-row softmax statistics of the acc tile and the target's acc
+  EPI_CE_GRAD = 9,     // g = (exp(acc - lse) - [target]) * scale: D = bf16(g), D2 = bf16(g - D)
+  EPI_CE_DZ = 10,      // D = bf16(acc + rem[m] * B[target[m]])  (rem as EPI_CE_GRAD left it)
 };
 
 // Epilogues that read a bf16 tile R, and those that write the activation pair.
@@ -22,6 +25,26 @@ constexpr bool epi_reads_r(int e) {
   return e == EPI_BF16_RESID || e == EPI_DRELU2 || e == EPI_DLRELU2;
 }
 constexpr bool epi_act_fwd(int e) { return e == EPI_RELU2 || e == EPI_LRELU2; }
+constexpr bool epi_ce(int e) { return e == EPI_CE_STATS || e == EPI_CE_GRAD || e == EPI_CE_DZ; }
+
+// Per-row inputs and outputs of the cross-entropy epilogues (row m of A is a
+// token; in STATS and GRAD column n of the product is the logit of word n).
+struct CeArgs {
+  const int64_t* targets = nullptr;  // [M]; outside [0, vocab): the row has no target
+  int vocab = 0;
+  const float* lse = nullptr;        // GRAD: [M] log-sum-exp of the logits
+  const float* dloss = nullptr;      // GRAD: [M] upstream gradient (null: 1)
+  const float* gscale = nullptr;     // GRAD: one factor of every row (null: 1)
+  float2* stats = nullptr;           // STATS: [ce_slots(M, N)][M] (max, sum of exp(logit - max))
+  float* tlogit = nullptr;           // STATS: [M], written where the row has a target
+  // GRAD writes, DZ reads, where the row has a target: what bf16 rounding left
+  // of g at the target.  That element is the row's largest, and with the mean's
+  // 1 / count in it nearly the same for all rows, so its rounding error is
+  // common to them instead of averaging out: dZ of a 50,257-word head was
+  // 2e-3 to 3.5e-3 off without the remainder.
+  float* rem = nullptr;              // [M]
+  const __nv_bfloat16* words = nullptr;  // DZ: the operand [vocab, N], rows N apart
+};
 
 // D[M,N] = A[M,K] . B[N,K]^T with bf16 operands and fp32 accumulation.
 // A is K-major (row m contiguous along K, row stride lda) unless a_mn, in which
@@ -43,6 +66,10 @@ struct GemmDesc {
   const void* R = nullptr;
   int64_t ldr = 0;
   bool accumulate = false;  // fp32 epilogues: add into D instead of overwriting
+  // fp32 epilogues: longest run of K that one accumulator sums (0: no limit).
+  // The tensor core's fp32 accumulation truncates at every step, so a sum over
+  // very long K drifts; runs are added to D in 32 bits, rounded to nearest.
+  int64_t k_run = 0;
   // Fused quantizing B producer: when set, B / ldb are ignored and the kernel
   // builds the bf16 operand bf16(fl32(c * s)) of this fp32 weight [N,K]
   // (row-major, ld = K) on the grid `bits` in shared memory -- the quantized
@@ -50,7 +77,11 @@ struct GemmDesc {
   // fused_b_supported() only.
   const float* Wraw = nullptr;
   int bits = 0;
+  CeArgs ce;  // cross-entropy epilogues
 };
+
+// Partial statistics per row that EPI_CE_STATS writes for an M x N product.
+int64_t ce_slots(int64_t M, int64_t N);
 
 // Whether launch_gemm can quantize B inside the GEMM for this shape / epilogue.
 bool fused_b_supported(int64_t M, int64_t N, int64_t K, int epi);

@@ -1,0 +1,26 @@
+// Host interfaces of the language-model operators beside the linears: the
+// softmax cross entropy's reductions, rotary positions and attention.
+#pragma once
+
+#include "common.cuh"
+
+namespace qat {
+
+// ---- cross entropy: joins the partial softmax statistics of each token
+// (slots x T pairs, see CeArgs) into lse and loss; with `mean`, also the mean
+// loss over the tokens that have a target and 1 / their count (0, 0 if none).
+struct CeJoin {
+  const float2* stats;
+  const float* tlogit;
+  const int64_t* targets;
+  float* loss;
+  float* lse;
+  float* mean;  // [2], nullable
+  void* parts;  // ce_parts_bytes(T), 16-byte aligned (only with mean)
+  int64_t T;
+  int slots, vocab;
+};
+int64_t ce_parts_bytes(int64_t T);
+int launch_ce_join(const CeJoin& j, cudaStream_t stream);
+
+}  // namespace qat

@@ -18,6 +18,7 @@ QAT_OK = 0
 QAT_ERR_ARG, QAT_ERR_ALIGN, QAT_ERR_SHAPE, QAT_ERR_WORKSPACE = 1, 2, 3, 4
 QAT_ERR_CUDA, QAT_ERR_TIMEOUT, QAT_ERR_UNSUPPORTED = 5, 6, 7
 QAT_OP_LINEAR_FWD, QAT_OP_LINEAR_BWD, QAT_OP_MLP_FWD, QAT_OP_MLP_BWD = 1, 2, 3, 4
+QAT_OP_CE_FWD, QAT_OP_CE_BWD, QAT_OP_ATTN_BWD = 5, 6, 7
 QAT_EXPORT_FP16 = 16
 QAT_EXPORT_MAX_DESCS = 256
 QAT_DTYPE_F32, QAT_DTYPE_BF16 = 0, 1
@@ -27,7 +28,8 @@ EXPORTED = ("qat_strerror", "qat_launch_count", "qat_device_error", "qat_quantiz
             "qat_workspace_size", "qat_linear_fwd", "qat_linear_bwd", "qat_mlp_fwd",
             "qat_mlp_bwd", "quantize_rows_export", "quantize_export_batch", "dequantize_rows",
             "qat_linear_fwd_noalloc", "qat_noisy_operand", "unpack_codes6",
-            "qat_quantize_weights_batch", "qat_selftest_wait_timeout", "dequantize_rows_batch")
+            "qat_quantize_weights_batch", "qat_selftest_wait_timeout", "dequantize_rows_batch",
+            "qat_ce_fwd", "qat_ce_bwd")
 QAT_EXPORT_PACK6 = 1
 QAT_EXPORT_CLIP_SEARCH = 2
 QAT_ACT_RELU2 = 0
@@ -105,6 +107,8 @@ def lib():
         L.qat_linear_fwd_noalloc.argtypes = [P, I32, I32, I32, P, I64, I64, P, P, P]
         L.qat_noisy_operand.argtypes = [P, I32, I32, I32, ctypes.c_uint64, ctypes.c_uint64, P, P,
                                         P]
+        L.qat_ce_fwd.argtypes = [P, P, I32, I32, I32, P, I64, I64, P, P, P, P, P, SZ, P]
+        L.qat_ce_bwd.argtypes = [P, P, I32, I32, I32, P, I64, I64, P, P, P, P, P, P, I32, P, SZ, P]
         for name in EXPORTED:
             if name not in ("qat_strerror", "qat_launch_count", "qat_workspace_size"):
                 getattr(L, name).restype = ctypes.c_int
@@ -349,3 +353,80 @@ def qat_linear_fwd_noalloc(W, X, Y, bits, residual=None, ldx=0, T=None, stream=N
         T = X.shape[0]
     _check(lib().qat_linear_fwd_noalloc(_p(W), N, K, bits, _p(X), ldx, T, _p(residual), _p(Y),
                                         _stream(stream)), "qat_linear_fwd_noalloc")
+
+
+# ------------------------------------------------ cross entropy, rotary, attention
+
+_FLOAT = {torch.float32: "fp32", torch.bfloat16: "bf16"}
+
+
+def _need(where, *specs):
+    """Refuses what the C side cannot see from a pointer: specs are (tensor or
+    None, dtype, elements at least); every tensor on the current CUDA device."""
+    cur = None
+    for t, dtype, n in specs:
+        if t is None:
+            continue
+        if not t.is_cuda or t.dtype != dtype or t.numel() < n:
+            raise QatError(QAT_ERR_ARG, where)
+        if cur is None:
+            cur = torch.cuda.current_device()
+        if t.device.index != cur:
+            raise QatError(QAT_ERR_ARG, where)
+
+
+def _rows(where, t, cols, T=None, ld=0):
+    """Row stride of a 2-D tensor whose rows hold at least `cols` contiguous elements."""
+    if t.dim() != 2 or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise QatError(QAT_ERR_ARG, where)
+    if T is not None and t.shape[0] < T:
+        raise QatError(QAT_ERR_ARG, where)
+    if ld == 0:
+        ld = t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0))
+    return ld
+
+
+def _head(where, W, qw):
+    if (W is None) == (qw is None):
+        raise QatError(QAT_ERR_ARG, where)
+    V, d = W.shape if qw is None else (qw.N, qw.K)
+    w, dt = (W, torch.float32) if qw is None else (qw.operand, torch.bfloat16)
+    _need(where, (w, dt, V * d))
+    if not w.is_contiguous():
+        raise QatError(QAT_ERR_ARG, where)
+    return V, d
+
+
+def qat_ce_fwd(Z, targets, loss, lse, bits, W=None, qw=None, mean=None, workspace=None,
+               stream=None):
+    """Softmax cross entropy of logits Z . Wq^T against int64 targets [T] (outside
+    [0, V): not counted); loss, lse [T] fp32, mean [2] fp32 = (mean loss, 1 / counted).
+    Z [T, d] bf16 may be a column range of wider rows."""
+    f, f32 = "qat_ce_fwd", torch.float32
+    V, d = _head(f, W, qw)
+    T = Z.shape[0]
+    ldz = _rows(f, Z, d)
+    _need(f, (Z, torch.bfloat16, 0), (targets, torch.int64, T), (loss, f32, T), (lse, f32, T),
+          (mean, f32, 2))
+    ws, wsb = _ws(workspace)
+    _check(lib().qat_ce_fwd(_p(W), _qref(qw), V, d, bits, _p(Z), ldz, T, _p(targets), _p(loss),
+                            _p(lse), _p(mean), ws, wsb, _stream(stream)), f)
+
+
+def qat_ce_bwd(Z, targets, lse, bits, W=None, qw=None, dloss=None, gscale=None, dZ=None, dW=None,
+               accumulate_dW=False, workspace=None, stream=None):
+    """g = (softmax - onehot) * dloss[t] * gscale; dZ = bf16(g . Wq) [T, d], dW (+)= g^T . Z
+    [V, d] fp32."""
+    f, f32 = "qat_ce_bwd", torch.float32
+    V, d = _head(f, W, qw)
+    T = Z.shape[0]
+    ldz = _rows(f, Z, d)
+    _need(f, (Z, torch.bfloat16, 0), (targets, torch.int64, T), (lse, f32, T), (dloss, f32, T),
+          (gscale, f32, 1), (dZ, torch.bfloat16, T * d), (dW, f32, V * d))
+    for t in (targets, lse, dloss, dZ, dW):
+        if t is not None and not t.is_contiguous():
+            raise QatError(QAT_ERR_ARG, f)
+    ws, wsb = _ws(workspace)
+    _check(lib().qat_ce_bwd(_p(W), _qref(qw), V, d, bits, _p(Z), ldz, T, _p(targets), _p(lse),
+                            _p(dloss), _p(gscale), _p(dZ), _p(dW), int(bool(accumulate_dW)), ws,
+                            wsb, _stream(stream)), f)
