@@ -246,6 +246,43 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
                const float* dloss, const float* gscale, qat_bf16* dZ, float* dW,
                int32_t accumulate_dW, void* workspace, size_t ws_bytes, qat_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions of queries and keys.  The first `rotary` dimensions of each
+ * head are taken in pairs -- (i, i + rotary/2), or (2i, 2i + 1) with
+ * interleaved != 0 -- and pair i of a token at position n is turned by
+ * 2 pi n freqs[i]:  a' = scale (a cos - b sin),  b' = scale (a sin + b cos);
+ * the other dimensions stay as they are.  inverse != 0 turns the other way:
+ * with the same scale that is the gradient (the transpose of the rotation).
+ * X, Y [T, heads * head_dim] fp32 or bf16 (dtype), rows ldx / ldy elements
+ * apart (multiples of 8; 0 -> heads * head_dim): the heads may be a column
+ * range of a wider row, such as the query and key columns of a Q|K|V
+ * projection.  Y may be X itself (same stride); otherwise they must not
+ * overlap.  head_dim a multiple of 8; rotary even, at most head_dim and
+ * QAT_ROPE_MAX_DIMS.  positions [T] int64 (any value), or NULL: row t is at
+ * t mod seq_len, or at t with seq_len = 0.  freqs [rotary / 2] fp64, turns per
+ * position: angles are reduced to a part of a turn in fp64, so far positions
+ * keep fp32's accuracy.  The rotation is computed in fp32 and rounded once.
+ * ------------------------------------------------------------------------- */
+#define QAT_ROPE_MAX_DIMS 1024
+int qat_rope(const void* X, int64_t ldx, void* Y, int64_t ldy, int32_t dtype, int64_t T,
+             int32_t heads, int32_t head_dim, int32_t rotary, const double* freqs, float scale,
+             const int64_t* positions, int64_t seq_len, int32_t interleaved, int32_t inverse,
+             qat_stream_t stream);
+
+/* HOST function: fills freqs [rotary / 2] (host memory, to be copied to the
+ * device once) and *scale for qat_rope.
+ *   PLAIN   freqs[i] = base^(-2i/rotary) / 2 pi
+ *   LINEAR  those divided by factor (positions squeezed into the trained length)
+ *   NTK     base multiplied by factor^(rotary / (rotary - 2))
+ *   YARN    pairs that make more than beta_fast turns over trained_len positions
+ *           stay, those that make fewer than beta_slow are divided by factor,
+ *           a linear ramp over the pair numbers between; scale = 0.1 ln factor + 1
+ * factor >= 1 (not read by PLAIN); trained_len and the betas are read by YARN. */
+enum { QAT_ROPE_PLAIN = 0, QAT_ROPE_LINEAR = 1, QAT_ROPE_NTK = 2, QAT_ROPE_YARN = 3 };
+int qat_rope_freqs(int32_t rotary, double base, int32_t scaling, double factor,
+                   int64_t trained_len, double beta_fast, double beta_slow, double* freqs,
+                   double* scale);
+
 /* Diagnostic (the pages have no counterpart): runs the library's bounded
  * device wait on a barrier that nothing arrives on, with a limit of limit_ns
  * (1 us .. 10 s, else QAT_ERR_ARG).  The wait gives up, records

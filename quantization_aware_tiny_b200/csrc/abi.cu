@@ -2,6 +2,7 @@
 // host, workspace carving, and the sequencing of quantizer and GEMM launches.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "gemm_sm100.cuh"
@@ -662,6 +663,79 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
     }
   }
   return QAT_OK;
+}
+
+int qat_rope_freqs(int32_t rotary, double base, int32_t scaling, double factor,
+                   int64_t trained_len, double beta_fast, double beta_slow, double* freqs,
+                   double* scale) {
+  if (!freqs || !scale || rotary <= 0 || (rotary & 1) || !(base > 1.0) || !std::isfinite(base))
+    return QAT_ERR_ARG;
+  if (scaling != QAT_ROPE_PLAIN && scaling != QAT_ROPE_LINEAR && scaling != QAT_ROPE_NTK &&
+      scaling != QAT_ROPE_YARN)
+    return QAT_ERR_ARG;
+  if (scaling != QAT_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return QAT_ERR_ARG;
+  if (scaling == QAT_ROPE_YARN && (trained_len <= 0 || !(beta_slow > 0.0) || !(beta_fast > beta_slow)))
+    return QAT_ERR_ARG;
+  if (rotary > QAT_ROPE_MAX_DIMS) return QAT_ERR_SHAPE;
+  const double two_pi = 6.283185307179586476925;
+  const int n = rotary / 2;
+  *scale = 1.0;
+  if (scaling == QAT_ROPE_NTK && rotary > 2) base *= std::pow(factor, rotary / (rotary - 2.0));
+  for (int i = 0; i < n; ++i) {
+    freqs[i] = std::pow(base, -2.0 * i / rotary) / two_pi;
+    if (scaling == QAT_ROPE_LINEAR) freqs[i] /= factor;
+  }
+  if (scaling == QAT_ROPE_YARN) {
+    // the pair number that makes `turns` whole turns over the trained length
+    auto pair_of = [&](double turns) {
+      return rotary * std::log(trained_len / (turns * two_pi)) / (2.0 * std::log(base));
+    };
+    const double low = std::max(std::floor(pair_of(beta_fast)), 0.0);
+    const double high = std::min(std::ceil(pair_of(beta_slow)), rotary - 1.0);
+    for (int i = 0; i < n; ++i) {
+      const double ramp =
+          std::min(std::max((i - low) / std::max(high - low, 0.001), 0.0), 1.0);
+      freqs[i] = freqs[i] * (1.0 - ramp) + freqs[i] / factor * ramp;
+    }
+    *scale = 0.1 * std::log(factor) + 1.0;
+  }
+  return QAT_OK;
+}
+
+int qat_rope(const void* X, int64_t ldx, void* Y, int64_t ldy, int32_t dtype, int64_t T,
+             int32_t heads, int32_t head_dim, int32_t rotary, const double* freqs, float scale,
+             const int64_t* positions, int64_t seq_len, int32_t interleaved, int32_t inverse,
+             qat_stream_t stream) {
+  if (T < 0 || heads <= 0 || seq_len < 0 || !freqs || (T > 0 && (!X || !Y))) return QAT_ERR_ARG;
+  if (dtype != QAT_DTYPE_F32 && dtype != QAT_DTYPE_BF16) return QAT_ERR_ARG;
+  if (!dim_ok(head_dim) || heads > (1 << 20) || rotary <= 0 || (rotary & 1) || rotary > head_dim ||
+      rotary > QAT_ROPE_MAX_DIMS)
+    return QAT_ERR_SHAPE;
+  const int64_t width = static_cast<int64_t>(heads) * head_dim;
+  if (ldx == 0) ldx = width;
+  if (ldy == 0) ldy = width;
+  if (width > (1 << 24) || ldx < width || ldy < width || (ldx & 7) || (ldy & 7)) return QAT_ERR_SHAPE;
+  if (!aligned_to(freqs, 8) || !aligned_to(positions, 8)) return QAT_ERR_ALIGN;
+  if (T == 0) return QAT_OK;
+  if (!aligned16(X) || !aligned16(Y)) return QAT_ERR_ALIGN;
+  if (X == Y && ldx != ldy) return QAT_ERR_ARG;
+  RopeArgs r{};
+  r.X = X;
+  r.Y = Y;
+  r.ldx = ldx;
+  r.ldy = ldy;
+  r.T = T;
+  r.positions = positions;
+  r.seq_len = seq_len;
+  r.freqs = freqs;
+  r.scale = scale;
+  r.heads = heads;
+  r.head_dim = head_dim;
+  r.rotary = rotary;
+  r.interleaved = interleaved != 0;
+  r.inverse = inverse != 0;
+  r.copy_rest = X != Y;
+  return launch_rope(r, dtype == QAT_DTYPE_BF16, stream);
 }
 
 }  // extern "C"

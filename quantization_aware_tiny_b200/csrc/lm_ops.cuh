@@ -23,4 +23,18 @@ struct CeJoin {
 int64_t ce_parts_bytes(int64_t T);
 int launch_ce_join(const CeJoin& j, cudaStream_t stream);
 
+// ---- rotary positions (row strides in elements; Y may equal X)
+struct RopeArgs {
+  const void* X;
+  void* Y;
+  int64_t ldx, ldy, T;
+  const int64_t* positions;  // [T], or null: the row's number modulo seq_len (0: not wrapped)
+  int64_t seq_len;
+  const double* freqs;       // [rotary / 2] turns per position
+  float scale;
+  int heads, head_dim, rotary, interleaved, inverse;
+  int copy_rest;             // Y is another tensor: the unrotated dimensions are copied
+};
+int launch_rope(const RopeArgs& r, bool bf16, cudaStream_t stream);
+
 }  // namespace qat

@@ -29,12 +29,14 @@ EXPORTED = ("qat_strerror", "qat_launch_count", "qat_device_error", "qat_quantiz
             "qat_mlp_bwd", "quantize_rows_export", "quantize_export_batch", "dequantize_rows",
             "qat_linear_fwd_noalloc", "qat_noisy_operand", "unpack_codes6",
             "qat_quantize_weights_batch", "qat_selftest_wait_timeout", "dequantize_rows_batch",
-            "qat_ce_fwd", "qat_ce_bwd")
+            "qat_ce_fwd", "qat_ce_bwd", "qat_rope", "qat_rope_freqs")
 QAT_EXPORT_PACK6 = 1
 QAT_EXPORT_CLIP_SEARCH = 2
 QAT_ACT_RELU2 = 0
 QAT_ACT_LEAKY_RELU2 = 1
 _ACTS = {"relu2": QAT_ACT_RELU2, "leaky2": QAT_ACT_LEAKY_RELU2}
+QAT_ROPE_MAX_DIMS = 1024
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 QAT_NOALLOC_MAX_ELEMS = 4194304
 QAT_NOALLOC_MAX_ROWS = 16384
 
@@ -109,6 +111,9 @@ def lib():
                                         P]
         L.qat_ce_fwd.argtypes = [P, P, I32, I32, I32, P, I64, I64, P, P, P, P, P, SZ, P]
         L.qat_ce_bwd.argtypes = [P, P, I32, I32, I32, P, I64, I64, P, P, P, P, P, P, I32, P, SZ, P]
+        F64, F32 = ctypes.c_double, ctypes.c_float
+        L.qat_rope.argtypes = [P, I64, P, I64, I32, I64, I32, I32, I32, P, F32, P, I64, I32, I32, P]
+        L.qat_rope_freqs.argtypes = [I32, F64, I32, F64, I64, F64, F64, P, P]
         for name in EXPORTED:
             if name not in ("qat_strerror", "qat_launch_count", "qat_workspace_size"):
                 getattr(L, name).restype = ctypes.c_int
@@ -430,3 +435,37 @@ def qat_ce_bwd(Z, targets, lse, bits, W=None, qw=None, dloss=None, gscale=None, 
     _check(lib().qat_ce_bwd(_p(W), _qref(qw), V, d, bits, _p(Z), ldz, T, _p(targets), _p(lse),
                             _p(dloss), _p(gscale), _p(dZ), _p(dW), int(bool(accumulate_dW)), ws,
                             wsb, _stream(stream)), f)
+
+
+def rope_freqs(rotary, base=10000.0, scaling="none", factor=1.0, trained_len=0, beta_fast=32.0,
+               beta_slow=1.0, device="cuda"):
+    """(freqs, scale) for qat_rope: turns per position of each rotated pair, a
+    float64 device tensor, and the factor of cos and sin.  scaling: "none",
+    "linear", "ntk" or "yarn" (contexts `factor` times the trained length)."""
+    if scaling not in _ROPE_SCALINGS or rotary < 2 or rotary % 2:
+        raise QatError(QAT_ERR_ARG, "rope_freqs")
+    f, m = (ctypes.c_double * (rotary // 2))(), ctypes.c_double(1.0)
+    _check(lib().qat_rope_freqs(rotary, base, _ROPE_SCALINGS[scaling], factor, int(trained_len),
+                                beta_fast, beta_slow, ctypes.cast(f, ctypes.c_void_p),
+                                ctypes.cast(ctypes.byref(m), ctypes.c_void_p)), "rope_freqs")
+    return torch.tensor(list(f), dtype=torch.float64, device=device), m.value
+
+
+def qat_rope(X, Y, heads, head_dim, freqs, positions=None, seq_len=0, interleaved=False, scale=1.0,
+             inverse=False, stream=None):
+    """Rotary positions of X [T, >= heads * head_dim] (fp32 or bf16, rows of any
+    stride) into Y (may be X); rotates the first 2 * len(freqs) dimensions of
+    each head.  inverse=True is the backward."""
+    f = "qat_rope"
+    T, width = X.shape[0], heads * head_dim
+    if X.dtype not in _FLOAT:
+        raise QatError(QAT_ERR_ARG, f)
+    ldx, ldy = _rows(f, X, width), _rows(f, Y, width, T)
+    _need(f, (X, X.dtype, 0), (Y, X.dtype, 0), (freqs, torch.float64, 1), (positions, torch.int64, T))
+    for t in (freqs, positions):
+        if t is not None and not t.is_contiguous():
+            raise QatError(QAT_ERR_ARG, f)
+    dt = QAT_DTYPE_BF16 if X.dtype == torch.bfloat16 else QAT_DTYPE_F32
+    _check(lib().qat_rope(_p(X), ldx, _p(Y), ldy, dt, T, heads, head_dim, 2 * freqs.numel(),
+                          _p(freqs), float(scale), _p(positions), int(seq_len),
+                          int(bool(interleaved)), int(bool(inverse)), _stream(stream)), f)

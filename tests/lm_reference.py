@@ -22,6 +22,23 @@ def contraction_error(n):
     return (n // 16 + 4) * 2 * E
 
 
+# ------------------------------------------------------------------- rotary
+
+def rotate(x, heads, head_dim, freqs, pos, interleaved, scale, inverse):
+    """x [T, heads * head_dim] float64 rotated, and the bound's pair magnitudes."""
+    T, rot = x.shape[0], 2 * freqs.numel()
+    y, mag = x.reshape(T, heads, head_dim).clone(), torch.zeros(T, heads, head_dim).double()
+    turns = pos.double()[:, None] * freqs[None]
+    ang = (turns - turns.round()) * (2 * math.pi) * (-1 if inverse else 1)
+    c, s = scale * ang.cos()[:, None], scale * ang.sin()[:, None]
+    i = torch.arange(rot // 2)
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
+    u, v = y[..., a].clone(), y[..., b].clone()
+    y[..., a], y[..., b] = u * c - v * s, u * s + v * c
+    mag[..., a] = mag[..., b] = abs(scale) * (u.abs() + v.abs())
+    return y.reshape(T, -1), mag.reshape(T, -1)
+
+
 # ------------------------------------------------------------ cross entropy
 
 def cross_entropy(z, w, targets, dloss=None, gscale=1.0):

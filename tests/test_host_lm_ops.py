@@ -1,8 +1,10 @@
 """Host-side argument checks of the language-model operators' C entry points:
 every refusal happens before a launch, so none of this needs a GPU."""
 import ctypes
+import math
 
 import pytest
+import torch
 
 from quantization_aware_tiny_b200 import qat
 
@@ -67,3 +69,57 @@ def test_ce_workspace_sizes():
         assert qat.workspace_size(qat.QAT_OP_CE_BWD, V, d, T, True) >= b + V * d * 2
         assert b <= max(f, (1 << 30) + 256 * 4 * (V + 8) + (1 << 20))
     assert qat.workspace_size(qat.QAT_OP_CE_FWD, 64, 64, 0, False) == 0
+
+
+# ------------------------------------------------------------------- rotary
+
+def rope(X=A16, ldx=0, Y=ctypes.c_void_p(0x20000), ldy=0, dtype=1, T=4, heads=2, hd=64, rot=64, freqs=A16,
+         scale=1.0, pos=None, seq=0):
+    return L().qat_rope(X, ldx, Y, ldy, dtype, T, heads, hd, rot, freqs, scale, pos, seq, 0, 0, None)
+
+
+def test_rope_refusals():
+    before = qat.launch_count()
+    for rc, kw in ((qat.QAT_ERR_ARG, dict(X=None)), (qat.QAT_ERR_ARG, dict(Y=None)),
+                   (qat.QAT_ERR_ARG, dict(freqs=None)), (qat.QAT_ERR_ARG, dict(T=-1)),
+                   (qat.QAT_ERR_ARG, dict(heads=0)), (qat.QAT_ERR_ARG, dict(dtype=2)),
+                   (qat.QAT_ERR_ARG, dict(seq=-1)), (qat.QAT_ERR_SHAPE, dict(rot=63)),
+                   (qat.QAT_ERR_SHAPE, dict(rot=66)), (qat.QAT_ERR_SHAPE, dict(rot=0)),
+                   (qat.QAT_ERR_SHAPE, dict(hd=60, rot=60)), (qat.QAT_ERR_SHAPE, dict(ldx=120)),
+                   (qat.QAT_ERR_SHAPE, dict(ldy=132)),
+                   (qat.QAT_ERR_SHAPE, dict(hd=2048, rot=1026)), (qat.QAT_ERR_ALIGN, dict(X=ODD)),
+                   (qat.QAT_ERR_ALIGN, dict(Y=ODD)), (qat.QAT_ERR_ALIGN, dict(freqs=ODD)),
+                   (qat.QAT_ERR_ALIGN, dict(pos=ODD)),
+                   (qat.QAT_ERR_ARG, dict(Y=A16, ldx=128, ldy=136))):
+        assert rope(**kw) == rc, kw
+    assert rope(T=0, X=None, Y=None) == qat.QAT_OK
+    assert qat.launch_count() == before
+
+
+def test_rope_freqs_are_the_formulas():
+    """Plain and linear term by term; NTK keeps the first pair and slows the last by the
+    factor; YaRN keeps fast pairs, divides slow ones, and 1 is its own scaling."""
+    n = 32
+    plain, m = qat.rope_freqs(2 * n, 10000.0, device="cpu")
+    assert m == 1.0
+    for i in range(n):
+        assert float(plain[i]) == pytest.approx(10000.0 ** (-i / n) / (2 * math.pi), rel=1e-15)
+    lin, _ = qat.rope_freqs(2 * n, 10000.0, "linear", 4.0, device="cpu")
+    assert torch.equal(lin, plain / 4)
+    ntk, _ = qat.rope_freqs(2 * n, 10000.0, "ntk", 4.0, device="cpu")
+    assert float(ntk[0]) == float(plain[0])
+    assert float(ntk[-1]) == pytest.approx(float(plain[-1]) / 4, rel=1e-12)
+    yarn, m = qat.rope_freqs(2 * n, 10000.0, "yarn", 16.0, trained_len=1024, device="cpu")
+    assert m == pytest.approx(0.1 * math.log(16.0) + 1.0)
+    turns = plain * 1024
+    assert torch.equal(yarn[turns > 64], plain[turns > 64])
+    assert torch.allclose(yarn[turns < 0.5], plain[turns < 0.5] / 16, rtol=1e-15)
+    assert bool((yarn <= plain).all()) and bool((yarn >= plain / 16 * (1 - 1e-15)).all())
+    same, m = qat.rope_freqs(2 * n, 10000.0, "yarn", 1.0, trained_len=1024, device="cpu")
+    assert m == 1.0 and torch.allclose(same, plain, rtol=1e-15)
+    for bad in (dict(rotary=3), dict(rotary=0), dict(rotary=8, scaling="other"), dict(rotary=8, base=1.0),
+                dict(rotary=8, scaling="linear", factor=0.5), dict(rotary=8, scaling="yarn", factor=2.0),
+                dict(rotary=8, scaling="yarn", factor=2.0, trained_len=64, beta_fast=1.0, beta_slow=1.0),
+                dict(rotary=8, base=float("nan")), dict(rotary=1026)):
+        with pytest.raises(qat.QatError):
+            qat.rope_freqs(device="cpu", **bad)
