@@ -283,6 +283,43 @@ int qat_rope_freqs(int32_t rotary, double base, int32_t scaling, double factor,
                    int64_t trained_len, double beta_fast, double beta_slow, double* freqs,
                    double* scale);
 
+/* ---------------------------------------------------------------------------
+ * Attention over a batch of sequences, grouped queries, with the backward that
+ * recomputes the probabilities.  Query head h reads key / value head
+ * h / (heads / kv_heads):
+ *   S = scale Q K^T, P = softmax over the keys a query sees, O = P V,
+ *   lse = log sum exp S.
+ * Rows: Q, O [Tq, heads * head_dim], K, V [Tk, kv_heads * head_dim] bf16, rows
+ * ldq / ldo / ldk / ldv elements apart (multiples of 8; 0 -> contiguous), so
+ * they may be column ranges of one Q|K|V projection; lse [heads, Tq] fp32.
+ * Sequences: b holds query rows [cu_q[b], cu_q[b+1]) and key rows
+ * [cu_k[b], cu_k[b+1]) (device int32 [batch + 1], ascending; offsets are cut to
+ * the tensors), none longer than max_q / max_k (longer ones are left
+ * unfinished); or, with a NULL table, max_q (max_k) rows each and
+ * Tq = batch * max_q (Tk = batch * max_k).  Rows of no sequence are left as
+ * they are, and nothing that lies in them -- NaN included -- reaches another row.
+ * causal != 0: the last query of a sequence is aligned with its last key, query
+ * i of nq sees keys j <= i + nk - nq; with window > 0 (causal only) just the
+ * last `window` of these.  A query that sees no key gets O = 0, lse = -inf and
+ * no gradient.  scale > 0, or 0 for 1 / sqrt(head_dim).  head_dim a multiple of
+ * 8 up to 128.  Products and sums are fp32; P and dS are rounded to bf16 as
+ * operands of the second products.  The same inputs give the same bits.
+ * ------------------------------------------------------------------------- */
+#define QAT_ATTN_MAX_HEAD_DIM 128
+typedef struct qat_attn {
+  int64_t Tq, Tk;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int32_t batch, max_q, max_k;
+  int32_t heads, kv_heads, head_dim;
+  int32_t causal, window;
+  float scale;
+  int32_t reserved; /* 0 */
+  int64_t ldq, ldk, ldv, ldo;
+} qat_attn;
+int qat_attn_fwd(const qat_attn* a, const qat_bf16* Q, const qat_bf16* K, const qat_bf16* V,
+                 qat_bf16* O, float* lse, qat_stream_t stream);
+
 /* Diagnostic (the pages have no counterpart): runs the library's bounded
  * device wait on a barrier that nothing arrives on, with a limit of limit_ns
  * (1 us .. 10 s, else QAT_ERR_ARG).  The wait gives up, records

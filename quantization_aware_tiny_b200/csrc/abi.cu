@@ -103,6 +103,8 @@ int get_operand(const float* W, const qat_qweight* qw, int64_t N, int64_t K, int
   return rc;
 }
 
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
 // ---- softmax cross entropy
 constexpr int64_t kCeMaxVocab = 1 << 20;
 constexpr int64_t kCeMaxTokens = (1ll << 31) - 256;
@@ -132,7 +134,49 @@ size_t ce_bwd_bytes(int64_t V, int64_t rows) {
   return 2 * align_up(rows * ce_ldg(V) * 2) + align_up(rows * 4);
 }
 
-bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// ---- attention
+// The checks that both directions share; fills the kernels' arguments.
+int attn_args(const qat_attn* a, const qat_bf16* Q, const qat_bf16* K, const qat_bf16* V,
+              const qat_bf16* O, const float* lse, AttnArgs* out) {
+  if (!a || a->Tq < 0 || a->Tk < 0 || a->batch < 0 || a->max_q < 0 || a->max_k < 0) return QAT_ERR_ARG;
+  if (a->heads <= 0 || a->kv_heads <= 0 || a->heads % a->kv_heads || a->window < 0)
+    return QAT_ERR_ARG;
+  if (a->window > 0 && !a->causal) return QAT_ERR_ARG;
+  if (!std::isfinite(a->scale) || a->scale < 0.0f) return QAT_ERR_ARG;
+  if (a->head_dim <= 0 || (a->head_dim & 7) || a->head_dim > QAT_ATTN_MAX_HEAD_DIM || a->heads > 65536)
+    return QAT_ERR_SHAPE;
+  if (a->Tq > (1ll << 31) - 512 || a->Tk > (1ll << 31) - 512) return QAT_ERR_SHAPE;
+  if (!a->cu_q && a->Tq != static_cast<int64_t>(a->batch) * a->max_q) return QAT_ERR_ARG;
+  if (!a->cu_k && a->Tk != static_cast<int64_t>(a->batch) * a->max_k) return QAT_ERR_ARG;
+  if ((a->Tq > 0 && (!Q || !O || !lse)) || (a->Tk > 0 && (!K || !V))) return QAT_ERR_ARG;
+  const int64_t wq = static_cast<int64_t>(a->heads) * a->head_dim;
+  const int64_t wk = static_cast<int64_t>(a->kv_heads) * a->head_dim;
+  const int64_t ldq = a->ldq ? a->ldq : wq, ldo = a->ldo ? a->ldo : wq;
+  const int64_t ldk = a->ldk ? a->ldk : wk, ldv = a->ldv ? a->ldv : wk;
+  if (ldq < wq || ldo < wq || ldk < wk || ldv < wk || ((ldq | ldo | ldk | ldv) & 7))
+    return QAT_ERR_SHAPE;
+  if (std::max({ldq, ldo, ldk, ldv}) > (1ll << 38)) return QAT_ERR_SHAPE;  // the maps' stride field
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O)) return QAT_ERR_ALIGN;
+  if (!aligned_to(lse, 4) || !aligned_to(a->cu_q, 4) || !aligned_to(a->cu_k, 4)) return QAT_ERR_ALIGN;
+  AttnArgs p{};
+  p.Tq = a->Tq; p.Tk = a->Tk;
+  p.cu_q = a->cu_q; p.cu_k = a->cu_k;
+  p.batch = a->batch; p.max_q = a->max_q; p.max_k = a->max_k;
+  p.heads = a->heads; p.group = a->heads / a->kv_heads; p.hd = a->head_dim;
+  p.causal = a->causal != 0; p.window = a->window;
+  p.scale = a->scale != 0.0f ? a->scale : 1.0f / std::sqrt(static_cast<float>(a->head_dim));
+  p.Q = Q; p.K = K; p.V = V;
+  p.O = const_cast<qat_bf16*>(O);
+  p.lse = const_cast<float*>(lse);
+  p.ldq = ldq; p.ldk = ldk; p.ldv = ldv; p.ldo = ldo;
+  if (a->Tk == 0) {  // no key is ever loaded, but the maps need an address
+    p.K = p.V = Q;
+    p.ldk = p.ldv = ldq;
+  }
+  *out = p;
+  return QAT_OK;
+}
+
 
 }  // namespace
 }  // namespace qat
@@ -736,6 +780,15 @@ int qat_rope(const void* X, int64_t ldx, void* Y, int64_t ldy, int32_t dtype, in
   r.inverse = inverse != 0;
   r.copy_rest = X != Y;
   return launch_rope(r, dtype == QAT_DTYPE_BF16, stream);
+}
+
+int qat_attn_fwd(const qat_attn* a, const qat_bf16* Q, const qat_bf16* K, const qat_bf16* V,
+                 qat_bf16* O, float* lse, qat_stream_t stream) {
+  AttnArgs p;
+  const int rc = attn_args(a, Q, K, V, O, lse, &p);
+  if (rc) return rc;
+  if (p.Tq == 0 || p.batch == 0 || p.max_q == 0) return QAT_OK;
+  return launch_attn_fwd(p, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,176 @@
+// What the attention kernels share: arguments, sequences, masks, and the
+// tcgen05 forms beside the GEMM's (operand A in tensor memory, TMEM stores).
+#pragma once
+
+#include "lm_ops.cuh"
+#include "sm100_ptx.cuh"
+
+namespace qat {
+
+constexpr float kAttnLog2e = 1.4426950408889634f;
+
+// 2^x to about 2^-22 relative (the special-function unit; 0 for x = -inf).
+__device__ __forceinline__ float attn_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);  // .x = a (low half), .y = b
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// 3-D tiled load {64 dims, 1 head, box rows} of a [token][head][dim] tensor.
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst,
+                                            int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T: A's rows are TMEM lanes, two bf16 per column.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+// Each lane of the warp writes 32 / 16 consecutive columns of its own TMEM lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+// Each lane reads 16 consecutive columns of its own TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// A warp's bounded wait: the same answer in every lane, so a wait that runs out
+// never leaves part of a warp behind.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          int* err) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err));
+}
+
+// Register split of a warpgroup (all its warps call it).
+template <int N>
+__device__ __forceinline__ void set_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Synchronizes the `n` threads that name barrier `id` (1..15).
+__device__ __forceinline__ void named_sync(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+// ---- sequences
+struct Seq {
+  int64_t q0, k0;  // first query / key row
+  int nq, nk;      // rows
+};
+
+// Sequence b: [cu[b], cu[b+1]) of the packed rows, or rows of equal length.
+// Offsets outside the tensor are cut to it, so no table makes a kernel leave it.
+__device__ __forceinline__ Seq seq_of(const AttnArgs& p, int b) {
+  Seq s;
+  if (p.cu_q) {
+    const int64_t a = min(max(static_cast<int64_t>(p.cu_q[b]), int64_t{0}), p.Tq);
+    const int64_t e = min(max(static_cast<int64_t>(p.cu_q[b + 1]), a), p.Tq);
+    s.q0 = a;
+    s.nq = static_cast<int>(e - a);
+  } else {
+    s.q0 = static_cast<int64_t>(b) * p.max_q;
+    s.nq = p.max_q;
+  }
+  if (p.cu_k) {
+    const int64_t a = min(max(static_cast<int64_t>(p.cu_k[b]), int64_t{0}), p.Tk);
+    const int64_t e = min(max(static_cast<int64_t>(p.cu_k[b + 1]), a), p.Tk);
+    s.k0 = a;
+    s.nk = static_cast<int>(e - a);
+  } else {
+    s.k0 = static_cast<int64_t>(b) * p.max_k;
+    s.nk = p.max_k;
+  }
+  return s;
+}
+
+// Keys [lo, hi) that query i of a sequence sees: all of them, or with `causal`
+// those up to its own place (the last query is at the last key), at most the
+// last `window` of these.
+__device__ __forceinline__ void keys_of(const AttnArgs& p, const Seq& s, int i, int& lo, int& hi) {
+  lo = 0;
+  hi = s.nk;
+  if (p.causal) {
+    const int last = i + s.nk - s.nq;  // may be negative: no key at all
+    hi = min(hi, last + 1);
+    if (p.window > 0) lo = max(lo, last - p.window + 1);
+  }
+  hi = max(hi, 0);
+  lo = min(lo, hi);
+}
+
+// Bytes of a tile of `rows` rows and NC 64-dim chunks; chunk c starts at c * rows * 128.
+__host__ __device__ constexpr int tile_bytes(int rows, int nc) { return rows * 128 * nc; }
+
+// Clears rows [from, rows) of a staged tile (every 128-byte row lies in one
+// swizzle line, so whole rows need no unswizzling); all lanes of one warp.
+// Rows behind a sequence's end hold other sequences' values, or anything, and
+// a zero probability does not cancel a NaN there.
+template <int NC>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int rows, int from, int lane) {
+  const uint32_t base = smem_u32(tile);
+  const int n = (rows - from) * 8;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+    for (int i = lane; i < n; i += 32)
+      st_shared_v4(base + c * rows * 128 + from * 128 + i * 16, 0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// K-major operand descriptor of k-step kk (16 dims) of a staged tile of `rows` rows.
+__device__ __forceinline__ uint64_t kmajor_desc(const uint8_t* tile, int rows, int kk) {
+  return sw128_desc(smem_u32(tile) + (kk >> 2) * rows * 128 + (kk & 3) * 32, 16, 1024);
+}
+// MN-major descriptor (the contraction runs over the tile's rows) of rows 16 kk .. 16 kk + 15.
+__device__ __forceinline__ uint64_t rows_desc(const uint8_t* tile, int rows, int kk) {
+  return sw128_desc(smem_u32(tile) + kk * 2048, rows * 128, 1024);
+}
+
+}  // namespace qat

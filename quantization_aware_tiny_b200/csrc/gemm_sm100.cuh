@@ -5,6 +5,14 @@
 
 namespace qat {
 
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder (null when the driver has none).
+EncodeFn get_encode();
+
 // Epilogue applied to the fp32 accumulator tile.
 enum Epi : int {
   EPI_BF16 = 0,        // D = bf16(acc)

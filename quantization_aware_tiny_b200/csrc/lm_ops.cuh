@@ -37,4 +37,24 @@ struct RopeArgs {
 };
 int launch_rope(const RopeArgs& r, bool bf16, cudaStream_t stream);
 
+// ---- attention over packed or equal-length sequences.  Q, O, dO, dQ rows hold
+// `heads` heads of hd, K, V, dK, dV rows heads / group; strides in elements.
+struct AttnArgs {
+  int64_t Tq, Tk;
+  const int32_t* cu_q;  // [batch + 1] first rows, or null: sequences of max_q rows
+  const int32_t* cu_k;
+  int batch, max_q, max_k;
+  int heads, group, hd, causal, window;
+  float scale;
+  const void *Q, *K, *V, *dO;
+  void* O;
+  float* lse;    // [heads][Tq]
+  float* delta;  // [heads][Tq], backward: rowsum(dO * O)
+  void *dQ, *dK, *dV;
+  int64_t ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv;
+  int* err;
+};
+int launch_attn_fwd(AttnArgs a, cudaStream_t stream);
+int launch_attn_bwd(AttnArgs a, cudaStream_t stream);
+
 }  // namespace qat

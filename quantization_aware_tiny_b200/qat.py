@@ -29,7 +29,8 @@ EXPORTED = ("qat_strerror", "qat_launch_count", "qat_device_error", "qat_quantiz
             "qat_mlp_bwd", "quantize_rows_export", "quantize_export_batch", "dequantize_rows",
             "qat_linear_fwd_noalloc", "qat_noisy_operand", "unpack_codes6",
             "qat_quantize_weights_batch", "qat_selftest_wait_timeout", "dequantize_rows_batch",
-            "qat_ce_fwd", "qat_ce_bwd", "qat_rope", "qat_rope_freqs")
+            "qat_ce_fwd", "qat_ce_bwd", "qat_rope", "qat_rope_freqs",
+            "qat_attn_fwd")
 QAT_EXPORT_PACK6 = 1
 QAT_EXPORT_CLIP_SEARCH = 2
 QAT_ACT_RELU2 = 0
@@ -66,6 +67,16 @@ class _DequantDesc(ctypes.Structure):
 
 
 QAT_DEQUANT_MAX_DESCS = 256
+
+
+class _Attn(ctypes.Structure):
+    _fields_ = [("Tq", ctypes.c_int64), ("Tk", ctypes.c_int64), ("cu_q", ctypes.c_void_p),
+                ("cu_k", ctypes.c_void_p), ("batch", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_k", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64),
+                ("ldv", ctypes.c_int64), ("ldo", ctypes.c_int64)]
 
 
 class _ExportDesc(ctypes.Structure):
@@ -114,6 +125,7 @@ def lib():
         F64, F32 = ctypes.c_double, ctypes.c_float
         L.qat_rope.argtypes = [P, I64, P, I64, I32, I64, I32, I32, I32, P, F32, P, I64, I32, I32, P]
         L.qat_rope_freqs.argtypes = [I32, F64, I32, F64, I64, F64, F64, P, P]
+        L.qat_attn_fwd.argtypes = [P, P, P, P, P, P, P]
         for name in EXPORTED:
             if name not in ("qat_strerror", "qat_launch_count", "qat_workspace_size"):
                 getattr(L, name).restype = ctypes.c_int
@@ -469,3 +481,44 @@ def qat_rope(X, Y, heads, head_dim, freqs, positions=None, seq_len=0, interleave
     _check(lib().qat_rope(_p(X), ldx, _p(Y), ldy, dt, T, heads, head_dim, 2 * freqs.numel(),
                           _p(freqs), float(scale), _p(positions), int(seq_len),
                           int(bool(interleaved)), int(bool(inverse)), _stream(stream)), f)
+
+
+def _attn(where, Q, K, V, O, lse, heads, kv_heads, head_dim, causal, window, scale, cu_q, cu_k,
+          max_q, max_k):
+    """The descriptor of one attention call.  Without cu_k the keys lie as the
+    queries do; without a table the rows are sequences of max_q (max_k) each."""
+    bf, wq, wk = torch.bfloat16, heads * head_dim, kv_heads * head_dim
+    Tq, Tk = Q.shape[0], K.shape[0]
+    if cu_k is None and max_k == 0:
+        cu_k, max_k = cu_q, max_q
+    _need(where, (Q, bf, 0), (K, bf, 0), (V, bf, 0), (O, bf, 0), (lse, torch.float32, heads * Tq),
+          (cu_q, torch.int32, 1), (cu_k, torch.int32, 1))
+    for t in (lse, cu_q, cu_k):
+        if t is not None and not t.is_contiguous():
+            raise QatError(QAT_ERR_ARG, where)
+    if cu_q is not None:
+        batch = cu_q.numel() - 1
+    elif cu_k is not None:
+        batch = cu_k.numel() - 1
+    else:
+        batch = Tq // max_q if max_q > 0 else (Tk // max_k if max_k > 0 else 0)
+    if cu_k is not None and cu_k.numel() - 1 != batch:
+        raise QatError(QAT_ERR_ARG, where)
+    return _Attn(Tq, Tk, cu_q.data_ptr() if cu_q is not None else None,
+                 cu_k.data_ptr() if cu_k is not None else None, batch, max_q, max_k, heads,
+                 kv_heads, head_dim, int(bool(causal)), window, 0.0 if scale is None else scale, 0,
+                 _rows(where, Q, wq), _rows(where, K, wk), _rows(where, V, wk, Tk),
+                 _rows(where, O, wq, Tq))
+
+
+def qat_attn_fwd(Q, K, V, O, lse, heads, kv_heads, head_dim, causal=True, window=0, scale=None,
+                 cu_q=None, cu_k=None, max_q=0, max_k=0, stream=None):
+    """O = softmax(scale Q K^T) V and lse [heads, Tq] fp32, grouped queries.  Rows
+    [T, heads * head_dim] bf16 of any stride; sequences by cu_q / cu_k (int32
+    offsets [batch + 1], none longer than max_q / max_k), or max_q (max_k) rows
+    each.  Without cu_k and max_k the keys lie as the queries do."""
+    f = "qat_attn_fwd"
+    a = _attn(f, Q, K, V, O, lse, heads, kv_heads, head_dim, causal, window, scale, cu_q, cu_k,
+              max_q, max_k)
+    _check(lib().qat_attn_fwd(ctypes.byref(a), _p(Q), _p(K), _p(V), _p(O), _p(lse),
+                              _stream(stream)), f)

@@ -39,6 +39,72 @@ def rotate(x, heads, head_dim, freqs, pos, interleaved, scale, inverse):
     return y.reshape(T, -1), mag.reshape(T, -1)
 
 
+# ---------------------------------------------------------------- attention
+
+def attention(q, k, v, do, heads, kv_heads, hd, cu_q, cu_k, causal, window, scale):
+    """Float64 attention and gradients of packed sequences, with bounds.
+
+    Roundings counted: S is off by its fp32 accumulation (`se`), so a probability
+    by the relative amount `pe` (twice: numerator and sum), plus 2^-22 of the
+    exponential; P is rounded to bf16 before P V and P^T dO, dS before dS K and
+    dS^T Q, and every result once more.  Probabilities are formed against a
+    maximum at most 2^8 stale, which costs bf16 nothing (same relative step)."""
+    G, f = heads // kv_heads, lambda t: torch.zeros_like(t)
+    o, o_t, dq, dq_t = f(q), f(q), f(q), f(q)
+    dk, dk_t, dv, dv_t = f(k), f(k), f(v), f(v)
+    lse = torch.full((heads, q.shape[0]), float("nan"), dtype=torch.float64)
+    lse_t = torch.zeros_like(lse)
+    for b in range(len(cu_q) - 1):
+        rq, rk = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        nq, nk = cu_q[b + 1] - cu_q[b], cu_k[b + 1] - cu_k[b]
+        if nq == 0:
+            continue
+        keep = torch.ones(nq, nk, dtype=torch.bool)
+        if causal:
+            keep = keep.tril(nk - nq)
+            if window:
+                keep = keep.triu(nk - nq - window + 1)
+        for h in range(heads):
+            c = slice(h * hd, (h + 1) * hd)
+            ck = slice(h // G * hd, (h // G + 1) * hd)
+            a, kk, vv, dd = q[rq, c], k[rk, ck], v[rk, ck], do[rq, c]
+            s = torch.where(keep, scale * (a @ kk.T), torch.tensor(-math.inf).double())
+            if nk == 0:
+                lse[h, rq] = -math.inf
+                continue
+            lse[h, rq] = torch.logsumexp(s, 1)
+            p = torch.nan_to_num(torch.softmax(s, 1), nan=0.0)
+            sabs = torch.where(keep, scale * (a.abs() @ kk.abs().T), torch.zeros(()).double())
+            se = ((contraction_error(hd) + 4 * E) * sabs).amax(1, keepdim=True)  # one bound per row
+            pe = 2 * se + 64 * E * (1 + sabs.amax(1, keepdim=True))
+            lse_t[h, rq] = (se + 32 * E * (1 + sabs.amax(1, keepdim=True))).squeeze(1) + \
+                contraction_error(nk)
+            ov = p @ vv
+            o[rq, c] = ov
+            o_e = (pe + U + contraction_error(nk)) * (p @ vv.abs())
+            o_t[rq, c] = U * ov.abs() + (1 + U) * o_e
+            dv[rk, ck] += p.T @ dd
+            pd = p.T @ dd.abs()
+            dv_t[rk, ck] += (p * pe).T @ dd.abs() + (U + contraction_error(nq * G)) * pd
+            dp = dd @ vv.T
+            delta = (dd * ov).sum(1, keepdim=True)
+            # delta is formed from the rounded O, dP in fp32
+            de = (dd.abs() * o_t[rq, c]).sum(1, keepdim=True) + \
+                contraction_error(hd) * (dd.abs() * ov.abs()).sum(1, keepdim=True)
+            dpe = contraction_error(hd) * (dd.abs() @ vv.abs().T)
+            ds = p * (dp - delta)
+            ds_e = p * (dpe + de) + (pe + U + 4 * E) * ds.abs() + 2 * E * p * (dp.abs() + delta.abs())
+            dq[rq, c] = scale * (ds @ kk)
+            dq_t[rq, c] = U * dq[rq, c].abs() + (1 + U) * scale * (
+                ds_e @ kk.abs() + contraction_error(nk) * (ds.abs() @ kk.abs()))
+            dk[rk, ck] += scale * (ds.T @ a)
+            dk_t[rk, ck] += scale * (ds_e.T @ a.abs() + contraction_error(nq * G) * (ds.abs().T @ a.abs()))
+    dk_t = U * dk.abs() + (1 + U) * dk_t
+    dv_t = U * dv.abs() + (1 + U) * dv_t
+    return {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv, "o_tol": o_t, "lse_tol": lse_t,
+            "dq_tol": dq_t, "dk_tol": dk_t, "dv_tol": dv_t}
+
+
 # ------------------------------------------------------------ cross entropy
 
 def cross_entropy(z, w, targets, dloss=None, gscale=1.0):
