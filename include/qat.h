@@ -320,6 +320,18 @@ typedef struct qat_attn {
 int qat_attn_fwd(const qat_attn* a, const qat_bf16* Q, const qat_bf16* K, const qat_bf16* V,
                  qat_bf16* O, float* lse, qat_stream_t stream);
 
+/* Gradients of qat_attn_fwd from its inputs, O and lse (P is computed again):
+ *   dP = dO V^T, dS = P * (dP - rowsum(dO * O)),
+ *   dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO,
+ * dK and dV summed over the query heads of their group.  All bf16, rows ldd*
+ * elements apart (0 -> contiguous): dQ, dK, dV may be the column ranges of one
+ * gradient of a Q|K|V projection.  Rows of no sequence are left as they are.
+ * workspace: qat_workspace_size(QAT_OP_ATTN_BWD, heads, head_dim, Tq, 0) bytes. */
+int qat_attn_bwd(const qat_attn* a, const qat_bf16* dO, int64_t lddo, const qat_bf16* Q,
+                 const qat_bf16* K, const qat_bf16* V, const qat_bf16* O, const float* lse,
+                 qat_bf16* dQ, int64_t lddq, qat_bf16* dK, int64_t lddk, qat_bf16* dV, int64_t lddv,
+                 void* workspace, size_t ws_bytes, qat_stream_t stream);
+
 /* Diagnostic (the pages have no counterpart): runs the library's bounded
  * device wait on a barrier that nothing arrives on, with a limit of limit_ns
  * (1 us .. 10 s, else QAT_ERR_ARG).  The wait gives up, records

@@ -238,6 +238,8 @@ size_t qat_workspace_size(int32_t op, int32_t N_or_d, int32_t K_or_H, int64_t T,
       if (op == QAT_OP_CE_BWD && T > 0) n = std::max(n, ce_bwd_bytes(a, ce_rows_wanted(a, b, T)));
       return n + (raw_weights ? operand_bytes(a, b) : 0);
     }
+    case QAT_OP_ATTN_BWD:  // a = heads: rowsum(dO * O) of every query and head
+      return align_up(static_cast<size_t>(a) * T * 4);
     default:
       return 0;
   }
@@ -789,6 +791,39 @@ int qat_attn_fwd(const qat_attn* a, const qat_bf16* Q, const qat_bf16* K, const 
   if (rc) return rc;
   if (p.Tq == 0 || p.batch == 0 || p.max_q == 0) return QAT_OK;
   return launch_attn_fwd(p, stream);
+}
+
+int qat_attn_bwd(const qat_attn* a, const qat_bf16* dO, int64_t lddo, const qat_bf16* Q,
+                 const qat_bf16* K, const qat_bf16* V, const qat_bf16* O, const float* lse,
+                 qat_bf16* dQ, int64_t lddq, qat_bf16* dK, int64_t lddk, qat_bf16* dV, int64_t lddv,
+                 void* workspace, size_t ws_bytes, qat_stream_t stream) {
+  AttnArgs p;
+  const int rc = attn_args(a, Q, K, V, O, lse, &p);
+  if (rc) return rc;
+  if ((p.Tq > 0 && (!dO || !dQ)) || (p.Tk > 0 && (!dK || !dV))) return QAT_ERR_ARG;
+  const int64_t wq = static_cast<int64_t>(p.heads) * p.hd, wk = wq / p.group;
+  p.lddo = lddo ? lddo : wq;
+  p.lddq = lddq ? lddq : wq;
+  p.lddk = lddk ? lddk : wk;
+  p.lddv = lddv ? lddv : wk;
+  if (p.lddo < wq || p.lddq < wq || p.lddk < wk || p.lddv < wk ||
+      ((p.lddo | p.lddq | p.lddk | p.lddv) & 7) || p.lddo > (1ll << 38))
+    return QAT_ERR_SHAPE;
+  if (!aligned16(dO) || !aligned16(dQ) || !aligned16(dK) || !aligned16(dV) || !aligned16(workspace))
+    return QAT_ERR_ALIGN;
+  if (p.batch == 0) return QAT_OK;
+  Carver ws(workspace, ws_bytes);
+  p.delta = static_cast<float*>(ws.take(static_cast<size_t>(p.heads) * p.Tq * 4));
+  if (p.Tq > 0 && !p.delta) return QAT_ERR_WORKSPACE;
+  p.dO = dO;
+  p.dQ = dQ;
+  p.dK = dK;
+  p.dV = dV;
+  if (p.Tq == 0) {  // no query is ever loaded, but the maps need an address
+    p.Q = p.dO = K;
+    p.ldq = p.lddo = p.ldk;
+  }
+  return launch_attn_bwd(p, stream);
 }
 
 }  // extern "C"

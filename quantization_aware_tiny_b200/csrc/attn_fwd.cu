@@ -72,25 +72,8 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
   // late query blocks see most keys under a causal mask: they start first
   const int i0 = static_cast<int>(gridDim.y - 1 - blockIdx.y) * 2 * BQ;
   if (i0 >= sq.nq) return;
-  // key blocks [b0, b1) of each tile
-  int b0[2], b1[2];
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int first = i0 + w * BQ, last = min(first + BQ, sq.nq) - 1;
-    b0[w] = b1[w] = 0;
-    if (first < sq.nq) {
-      int lo, hi, lo2, hi2;
-      keys_of(p, sq, first, lo, hi);
-      keys_of(p, sq, last, lo2, hi2);
-      // the last row sees furthest; where the first sees nothing, a later one starts at key 0
-      b0[w] = hi > lo ? lo / BKV : 0;
-      b1[w] = hi2 > lo2 ? (hi2 + BKV - 1) / BKV : b0[w];
-    }
-  }
-  int j0 = b1[0] > b0[0] ? b0[0] : b0[1];
-  int j1 = max(b1[0], b1[1]);
-  if (b1[1] > b0[1]) j0 = min(j0, b0[1]);
-  if (j1 < j0) j1 = j0;
+  int b0[2], b1[2], j0, j1;
+  key_blocks<BQ, BKV>(p, sq, i0, b0, b1, j0, j1);
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -123,7 +106,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
   const int kv_head = head / p.group;
 
   if (warp < 4) {
-  set_regs_dec<C::REGS_ISSUE>();
+    set_regs_dec<C::REGS_ISSUE>();
   if (warp == 0) {
     if (lane == 0 && j1 > j0) {
       // ------------------------------------------------ TMA producer

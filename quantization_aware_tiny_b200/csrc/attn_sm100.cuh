@@ -94,11 +94,6 @@ __device__ __forceinline__ void set_regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Synchronizes the `n` threads that name barrier `id` (1..15).
-__device__ __forceinline__ void named_sync(int id, int n) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-
 // ---- sequences
 struct Seq {
   int64_t q0, k0;  // first query / key row
@@ -137,12 +132,47 @@ __device__ __forceinline__ void keys_of(const AttnArgs& p, const Seq& s, int i, 
   lo = 0;
   hi = s.nk;
   if (p.causal) {
-    const int last = i + s.nk - s.nq;  // may be negative: no key at all
-    hi = min(hi, last + 1);
-    if (p.window > 0) lo = max(lo, last - p.window + 1);
+    const int64_t last = static_cast<int64_t>(i) + s.nk - s.nq;  // negative: no key at all
+    hi = static_cast<int>(min(static_cast<int64_t>(hi), max(last + 1, int64_t{0})));
+    if (p.window > 0)
+      lo = static_cast<int>(min(max(last - p.window + 1, int64_t{0}), static_cast<int64_t>(hi)));
   }
-  hi = max(hi, 0);
+}
+
+// Queries [lo, hi) of a sequence that see key j (the same rule, read the other way).
+__device__ __forceinline__ void queries_of(const AttnArgs& p, const Seq& s, int j, int& lo, int& hi) {
+  lo = 0;
+  hi = s.nq;
+  if (p.causal) {
+    const int64_t same = static_cast<int64_t>(j) + s.nq - s.nk;  // the query at this key's place
+    lo = static_cast<int>(min(max(same, int64_t{0}), static_cast<int64_t>(s.nq)));
+    if (p.window > 0)
+      hi = static_cast<int>(min(max(same + p.window, int64_t{0}), static_cast<int64_t>(s.nq)));
+  }
   lo = min(lo, hi);
+}
+
+// Key blocks [b0[w], b1[w]) that tiles w = 0, 1 of ROWS queries from i0 on see,
+// and [j0, j1), which covers both; a tile that sees nothing has b1 = b0.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ void key_blocks(const AttnArgs& p, const Seq& s, int i0, int (&b0)[2],
+                                           int (&b1)[2], int& j0, int& j1) {
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int first = i0 + w * ROWS, last = min(first + ROWS, s.nq) - 1;
+    b0[w] = b1[w] = 0;
+    if (first < s.nq) {
+      int lo, hi, lo2, hi2;
+      keys_of(p, s, first, lo, hi);
+      keys_of(p, s, last, lo2, hi2);
+      // the last row sees furthest; where the first sees nothing, a later one starts at key 0
+      b0[w] = hi > lo ? lo / KEYS : 0;
+      b1[w] = hi2 > lo2 ? (hi2 + KEYS - 1) / KEYS : b0[w];
+    }
+  }
+  j0 = b1[0] > b0[0] ? b0[0] : b0[1];
+  if (b1[1] > b0[1]) j0 = min(j0, b0[1]);
+  j1 = max(max(b1[0], b1[1]), j0);
 }
 
 // Bytes of a tile of `rows` rows and NC 64-dim chunks; chunk c starts at c * rows * 128.

@@ -30,7 +30,7 @@ EXPORTED = ("qat_strerror", "qat_launch_count", "qat_device_error", "qat_quantiz
             "qat_linear_fwd_noalloc", "qat_noisy_operand", "unpack_codes6",
             "qat_quantize_weights_batch", "qat_selftest_wait_timeout", "dequantize_rows_batch",
             "qat_ce_fwd", "qat_ce_bwd", "qat_rope", "qat_rope_freqs",
-            "qat_attn_fwd")
+            "qat_attn_fwd", "qat_attn_bwd")
 QAT_EXPORT_PACK6 = 1
 QAT_EXPORT_CLIP_SEARCH = 2
 QAT_ACT_RELU2 = 0
@@ -126,6 +126,7 @@ def lib():
         L.qat_rope.argtypes = [P, I64, P, I64, I32, I64, I32, I32, I32, P, F32, P, I64, I32, I32, P]
         L.qat_rope_freqs.argtypes = [I32, F64, I32, F64, I64, F64, F64, P, P]
         L.qat_attn_fwd.argtypes = [P, P, P, P, P, P, P]
+        L.qat_attn_bwd.argtypes = [P, P, I64, P, P, P, P, P, P, I64, P, I64, P, I64, P, SZ, P]
         for name in EXPORTED:
             if name not in ("qat_strerror", "qat_launch_count", "qat_workspace_size"):
                 getattr(L, name).restype = ctypes.c_int
@@ -521,4 +522,19 @@ def qat_attn_fwd(Q, K, V, O, lse, heads, kv_heads, head_dim, causal=True, window
     a = _attn(f, Q, K, V, O, lse, heads, kv_heads, head_dim, causal, window, scale, cu_q, cu_k,
               max_q, max_k)
     _check(lib().qat_attn_fwd(ctypes.byref(a), _p(Q), _p(K), _p(V), _p(O), _p(lse),
+                              _stream(stream)), f)
+
+
+def qat_attn_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, heads, kv_heads, head_dim, causal=True, window=0,
+                 scale=None, cu_q=None, cu_k=None, max_q=0, max_k=0, workspace=None, stream=None):
+    """dQ, dK, dV of qat_attn_fwd from dO and what the forward read and wrote
+    (the other arguments as there).  All bf16, rows of any stride."""
+    f, bf, wq, wk = "qat_attn_bwd", torch.bfloat16, heads * head_dim, kv_heads * head_dim
+    a = _attn(f, Q, K, V, O, lse, heads, kv_heads, head_dim, causal, window, scale, cu_q, cu_k,
+              max_q, max_k)
+    _need(f, (dO, bf, 0), (dQ, bf, 0), (dK, bf, 0), (dV, bf, 0))
+    ws, wsb = _ws(workspace)
+    _check(lib().qat_attn_bwd(ctypes.byref(a), _p(dO), _rows(f, dO, wq, a.Tq), _p(Q), _p(K), _p(V),
+                              _p(O), _p(lse), _p(dQ), _rows(f, dQ, wq, a.Tq), _p(dK),
+                              _rows(f, dK, wk, a.Tk), _p(dV), _rows(f, dV, wk, a.Tk), ws, wsb,
                               _stream(stream)), f)

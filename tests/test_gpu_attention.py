@@ -72,6 +72,25 @@ class Case:
         within(got[:n, :width], ref, tol, what)
         assert bool((got[n:] == 7).all()) and bool((got[:, width:] == 7).all()), what + ": rows beside"
 
+    def backward(self, o, lse, **more):
+        wq, wk = self.heads * self.hd, self.kv_heads * self.hd
+        grads = self.out(self.nq, wq), self.out(self.nk, wk), self.out(self.nk, wk)
+        ws = torch.full((qat.workspace_size(qat.QAT_OP_ATTN_BWD, self.heads, self.hd, self.Q.shape[0], False),),
+                        255, dtype=torch.uint8, device="cuda")  # NaN
+        qat.qat_attn_bwd(self.dO, self.Q, self.K, self.V, o[:, :wq], lse, grads[0][:, :wq],
+                         grads[1][:, :wk], grads[2][:, :wk], self.heads, self.kv_heads, self.hd,
+                         workspace=ws, **{**self.kw(), **more})
+        return grads
+
+    def check_backward(self):
+        o, lse = self.forward()
+        grads = self.backward(o, lse)
+        torch.cuda.synchronize()
+        assert qat.device_error() == 0
+        r = self.reference()
+        for name, g, heads in zip(("dq", "dk", "dv"), grads, (self.heads, self.kv_heads, self.kv_heads)):
+            self.compare(g, heads * self.hd, r[name], r[name + "_tol"], name)
+
     def check_forward(self):
         o, lse = self.forward()
         torch.cuda.synchronize()
@@ -152,3 +171,159 @@ def test_fwd_offsets_past_32_bits():
     qat.qat_attn_fwd(big[:, :64], big[:, 64:128], big[:, 128:192], big[:, 192:256], lse2, 1, 1, 64, max_q=n)
     torch.cuda.synchronize()
     assert torch.equal(big[:, 192:256], want) and torch.equal(lse, lse2)
+
+
+# ------------------------------------------------------------------ backward
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_bwd_head_layouts(heads, causal):
+    h, kv, hd = heads
+    Case([200, 1, 129], heads=h, kv_heads=kv, hd=hd, causal=causal).check_backward()
+
+
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 383, 600])
+def test_bwd_lengths(n, mask):
+    Case([n], heads=2, kv_heads=1, **mask).check_backward()
+
+
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("lens", [([64, 64], [300, 129]), ([300, 1, 5], [64, 1, 0]), ([130], [129]),
+                                  ([1, 1, 1], [1, 200, 513]), ([0, 257, 0], [3, 257, 0])])
+def test_bwd_queries_and_keys_of_other_lengths(lens, mask):
+    Case(*lens, heads=2, kv_heads=2, hd=80, **mask).check_backward()
+
+
+def test_bwd_equal_lengths_without_tables():
+    Case([160] * 3, packed=False).check_backward()
+    Case([64] * 3, [200] * 3, packed=False, hd=128).check_backward()
+
+
+@pytest.mark.parametrize("peak", [0.0, 5.0])
+def test_bwd_flat_and_peaked_rows(peak):
+    Case([700], heads=1, kv_heads=1, peak=peak).check_backward()
+
+
+def test_bwd_scale():
+    Case([150], scale=0.7).check_backward()
+
+
+def test_bwd_no_keys_and_no_queries():
+    """Without keys dQ is zero, without queries dK and dV are."""
+    c = Case([5, 3], [0, 0])
+    c.check_backward()
+    Case([0, 0], [5, 3]).check_backward()
+
+
+def test_bwd_nan_of_another_sequence_stays_there():
+    c = Case([100, 70, 90], tail=0)
+    o, lse = c.forward()
+    want = c.backward(o, lse)
+    for t in (c.Q, c.K, c.V, c.dO):
+        t[100:170] = float("nan")
+    o, lse = c.forward()
+    got = c.backward(o, lse)
+    torch.cuda.synchronize()
+    keep = torch.ones(260, dtype=torch.bool, device="cuda")
+    keep[100:170] = False
+    for a, b in zip(want, got):
+        assert torch.equal(a[keep], b[keep])
+
+
+def test_bwd_gradients_into_one_projection_row():
+    """dQ, dK, dV as the column ranges of one buffer, bit for bit."""
+    c = Case([300], pad=0, tail=0)
+    o, lse = c.forward()
+    want = c.backward(o, lse)
+    dqkv = torch.empty(300, 512, dtype=BF, device="cuda")
+    ws = torch.empty(qat.workspace_size(qat.QAT_OP_ATTN_BWD, 4, 64, 300, False), dtype=torch.uint8, device="cuda")
+    qat.qat_attn_bwd(c.dO, c.Q, c.K, c.V, o, lse, dqkv[:, :256], dqkv[:, 256:384], dqkv[:, 384:], 4, 2, 64,
+                     workspace=ws, **c.kw())
+    torch.cuda.synchronize()
+    assert torch.equal(dqkv, torch.cat(want, 1))
+
+
+def test_bwd_against_differences():
+    """All three gradients along random directions against the difference quotient of
+    the float64 form's sum(O * dO)."""
+    c = Case([90, 33], heads=2, kv_heads=1, hd=24, pad=0, tail=0)
+    o, lse = c.forward()
+    grads = c.backward(o, lse)
+    torch.cuda.synchronize()
+    r, g = c.reference(), torch.Generator().manual_seed(5)
+    base = [f64(t) for t in (c.q, c.k, c.v)]
+    f = lambda x: float((attention(*x, f64(c.do), 2, 1, 24, c.cu_q, c.cu_k, True, 0, 24 ** -0.5)["o"] * f64(c.do)).sum())
+    for at, (name, got) in enumerate(zip(("dq", "dk", "dv"), grads)):
+        d, h = torch.randn(base[at].shape, generator=g).double(), 1e-5
+        move = lambda e: [x + e * d if n == at else x for n, x in enumerate(base)]
+        quotient = (f(move(h)) - f(move(-h))) / (2 * h)
+        assert abs(float((f64(got) * d).sum()) - quotient) <= float((r[name + "_tol"] * d.abs()).sum()) + 1e-5
+
+
+def test_same_bits_every_time_on_two_streams_and_in_a_graph():
+    """Two calls at once on their own streams and workspaces, and a captured forward
+    and backward replayed on new values while eager calls go on, give the eager bits."""
+    c, c2 = Case([500, 77], seed=1, tail=0, pad=0), Case([500, 77], seed=2, tail=0, pad=0)
+
+    def both(x):
+        o, lse = x.forward()
+        return (o, lse) + tuple(x.backward(o, lse))
+
+    want, want2 = both(c), both(c2)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            a = both(c)
+        with torch.cuda.stream(s2):
+            b = both(c2)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, a))
+        assert all(torch.equal(x, y) for x, y in zip(want2, b))
+    kw = c.kw()
+    c.kw = lambda: kw  # the tables are made once, outside the capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s1), torch.cuda.graph(graph, stream=s1):
+        got = both(c)
+    keep = [t.clone() for t in (c.Q, c.K, c.V, c.dO)]
+    for src, w in ((( c2.Q, c2.K, c2.V, c2.dO), want2), (keep, want)):
+        for t, x in zip((c.Q, c.K, c.V, c.dO), src):
+            t.copy_(x)
+        graph.replay()
+        both(c2)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(w, got))
+
+
+def test_refusals():
+    c = Case([64], tail=0, pad=0)
+    o, lse = c.forward()
+    ws = torch.empty(qat.workspace_size(qat.QAT_OP_ATTN_BWD, 4, 64, 64, False), dtype=torch.uint8, device="cuda")
+    kw = c.kw()
+
+    def bad(code, Q=c.Q, K=c.K, V=c.V, O=o, L=lse, heads=4, kv=2, hd=64, **k):
+        with pytest.raises(qat.QatError) as e:
+            qat.qat_attn_fwd(Q, K, V, O, L, heads, kv, hd, **{**kw, **k})
+        assert e.value.code == code
+
+    before = qat.launch_count()
+    bad(qat.QAT_ERR_ARG, Q=c.Q.float())
+    bad(qat.QAT_ERR_ARG, K=c.K.half())
+    bad(qat.QAT_ERR_ARG, L=lse.double())
+    bad(qat.QAT_ERR_ARG, L=lse[:3])
+    bad(qat.QAT_ERR_ARG, O=o[:63])
+    bad(qat.QAT_ERR_ARG, V=c.V[:63])
+    bad(qat.QAT_ERR_ARG, Q=c.Q.cpu())
+    bad(qat.QAT_ERR_ARG, heads=8)
+    bad(qat.QAT_ERR_ARG, kv=3)
+    bad(qat.QAT_ERR_ARG, cu_q=kw["cu_q"].long())
+    bad(qat.QAT_ERR_ARG, cu_k=kw["cu_k"][:1])
+    bad(qat.QAT_ERR_ARG, causal=False, window=4)
+    bad(qat.QAT_ERR_ARG, cu_q=None, cu_k=None, max_q=60, max_k=60)
+    bad(qat.QAT_ERR_SHAPE, heads=2, kv=1, hd=60)
+    bad(qat.QAT_ERR_SHAPE, heads=1, kv=1, hd=136, K=torch.cat([c.K, c.K], 1), V=torch.cat([c.V, c.V], 1))
+    with pytest.raises(qat.QatError) as e:
+        qat.qat_attn_bwd(c.dO, c.Q, c.K, c.V, o, lse, o, c.K, c.V, 4, 2, 64, workspace=ws[:512], **kw)
+    assert e.value.code == qat.QAT_ERR_WORKSPACE
+    assert qat.launch_count() == before

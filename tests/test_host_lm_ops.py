@@ -123,3 +123,50 @@ def test_rope_freqs_are_the_formulas():
                 dict(rotary=8, base=float("nan")), dict(rotary=1026)):
         with pytest.raises(qat.QatError):
             qat.rope_freqs(device="cpu", **bad)
+
+
+# ---------------------------------------------------------------- attention
+
+def attn(Q=A16, K=A16, V=A16, O=A16, lse=A16, **kw):
+    d = dict(Tq=64, Tk=64, cu_q=None, cu_k=None, batch=1, max_q=64, max_k=64, heads=4, kv_heads=2,
+             head_dim=64, causal=1, window=0, scale=0.0, reserved=0, ldq=0, ldk=0, ldv=0, ldo=0)
+    grad = {k: kw.pop(k) for k in ("lddo", "lddq", "lddk", "lddv", "dO", "dQ", "dK", "dV", "ws", "wsb") if k in kw}
+    a = ctypes.byref(qat._Attn(**{**d, **kw}))
+    if not grad:
+        return L().qat_attn_fwd(a, Q, K, V, O, lse, None)
+    g = lambda k: grad.get(k, 0 if k.startswith("ld") else A16)
+    return L().qat_attn_bwd(a, g("dO"), g("lddo"), Q, K, V, O, lse, g("dQ"), g("lddq"), g("dK"), g("lddk"),
+                            g("dV"), g("lddv"), g("ws"), grad.get("wsb", BIG), None)
+
+
+def test_attention_refusals():
+    before = qat.launch_count()
+    nan, inf = float("nan"), float("inf")
+    cases = [(qat.QAT_ERR_ARG, dict(Q=None)), (qat.QAT_ERR_ARG, dict(K=None)), (qat.QAT_ERR_ARG, dict(V=None)),
+             (qat.QAT_ERR_ARG, dict(O=None)), (qat.QAT_ERR_ARG, dict(lse=None)), (qat.QAT_ERR_ARG, dict(Tq=-1)),
+             (qat.QAT_ERR_ARG, dict(heads=0)), (qat.QAT_ERR_ARG, dict(kv_heads=3)),
+             (qat.QAT_ERR_ARG, dict(kv_heads=0)), (qat.QAT_ERR_ARG, dict(window=-1)),
+             (qat.QAT_ERR_ARG, dict(window=3, causal=0)), (qat.QAT_ERR_ARG, dict(scale=nan)),
+             (qat.QAT_ERR_ARG, dict(scale=inf)), (qat.QAT_ERR_ARG, dict(scale=-1.0)),
+             (qat.QAT_ERR_ARG, dict(Tq=65)), (qat.QAT_ERR_ARG, dict(Tk=32)), (qat.QAT_ERR_ARG, dict(batch=-1)),
+             (qat.QAT_ERR_SHAPE, dict(head_dim=60)), (qat.QAT_ERR_SHAPE, dict(head_dim=136)),
+             (qat.QAT_ERR_SHAPE, dict(head_dim=0)), (qat.QAT_ERR_SHAPE, dict(ldq=248)),
+             (qat.QAT_ERR_SHAPE, dict(ldk=132)), (qat.QAT_ERR_SHAPE, dict(ldo=260)),
+             (qat.QAT_ERR_SHAPE, dict(ldv=1 << 40)),
+             (qat.QAT_ERR_SHAPE, dict(Tq=(1 << 31) - 1, batch=1, max_q=(1 << 31) - 1)),
+             (qat.QAT_ERR_ALIGN, dict(Q=ODD)), (qat.QAT_ERR_ALIGN, dict(lse=ODD)),
+             (qat.QAT_ERR_ALIGN, dict(cu_q=0x10002))]
+    for rc, kw in cases:
+        assert attn(**kw) == rc, kw
+        assert attn(dO=A16, **kw) == rc, kw
+    for rc, kw in ((qat.QAT_ERR_ARG, dict(dO=None)), (qat.QAT_ERR_ARG, dict(dQ=None)),
+                   (qat.QAT_ERR_ARG, dict(dK=None)), (qat.QAT_ERR_ARG, dict(dV=None)),
+                   (qat.QAT_ERR_SHAPE, dict(lddo=100)), (qat.QAT_ERR_SHAPE, dict(lddq=260)),
+                   (qat.QAT_ERR_SHAPE, dict(lddk=64)), (qat.QAT_ERR_ALIGN, dict(dV=ODD)),
+                   (qat.QAT_ERR_ALIGN, dict(ws=ODD)), (qat.QAT_ERR_WORKSPACE, dict(ws=None)),
+                   (qat.QAT_ERR_WORKSPACE, dict(wsb=4 * 64 * 4 - 1))):
+        assert attn(**kw) == rc, kw
+    # nothing to do: no sequences, no rows
+    assert attn(batch=0, Tq=0, Tk=0) == qat.QAT_OK and attn(dO=A16, batch=0, Tq=0, Tk=0) == qat.QAT_OK
+    assert attn(batch=3, Tq=0, max_q=0, Tk=192) == qat.QAT_OK
+    assert qat.launch_count() == before
