@@ -7,23 +7,80 @@ import torch
 from . import qat
 
 
+class CoreAttention:
+    """The attention of a core's block: `heads` query heads over `kv_heads` key
+    and value heads, causal (optionally the last `window` keys only), on
+    sequences of seq_len rows each, or packed ones given by cu (int32 row
+    offsets [batch + 1] on the device, none longer than seq_len).  rope, when
+    given, is (freqs, scale) of qat.rope_freqs: queries and keys are rotated,
+    by the row's place in its sequence, or by positions [T] int64 (needed with cu)."""
+
+    def __init__(self, heads, kv_heads, seq_len, cu=None, window=0, rope=None, positions=None,
+                 interleaved=False):
+        if rope is not None and cu is not None and positions is None:
+            raise ValueError("packed sequences need their rotary positions")
+        self.heads, self.kv_heads, self.seq_len = heads, kv_heads, seq_len
+        self.cu, self.window, self.rope = cu, window, rope
+        self.positions, self.interleaved = positions, interleaved
+
+    def split(self, x, hd):
+        """The query, key and value columns of a Q|K|V row tensor."""
+        q, k = self.heads * hd, (self.heads + self.kv_heads) * hd
+        return x[:, :q], x[:, q:k], x[:, k:]
+
+    def rotate(self, qkv, hd, inverse, stream):
+        """Rotary positions of the query and key columns, in place."""
+        if self.rope is None:
+            return
+        freqs, scale = self.rope
+        n = self.heads + self.kv_heads
+        qk = qkv[:, :n * hd]
+        qat.qat_rope(qk, qk, n, hd, freqs, positions=self.positions,
+                     seq_len=0 if self.positions is not None else self.seq_len,
+                     interleaved=self.interleaved, scale=scale, inverse=inverse, stream=stream)
+
+    def _kw(self, hd, stream):
+        return dict(heads=self.heads, kv_heads=self.kv_heads, head_dim=hd, window=self.window,
+                    cu_q=self.cu, max_q=self.seq_len, stream=stream)
+
+    def forward(self, qkv, att, lse, hd, stream):
+        """Rotates qkv in place and writes the attention output and lse."""
+        self.rotate(qkv, hd, False, stream)
+        qat.qat_attn_fwd(*self.split(qkv, hd), att, lse, **self._kw(hd, stream))
+
+    def backward(self, datt, qkv, att, lse, dqkv, ws, hd, stream):
+        """dqkv (of the unrotated projection) from the output's gradient."""
+        qat.qat_attn_bwd(datt, *self.split(qkv, hd), att, lse, *self.split(dqkv, hd), workspace=ws,
+                         **self._kw(hd, stream))
+        self.rotate(dqkv, hd, True, stream)
+
+
 class RecurrentCore:
     """Depth-recurrent core ("Depth Recurrence + Mixed-Precision Quant"
     write-up, "Stem / Core / Tail" and "税 1"): the block's weights are
     quantized ONCE (the cache) and its linears are applied R times.
 
-    Per application, attention left out (the O projection reads the query
-    slice of QKV in its place):
+    Per application:
         qkv = x Wqkv^T              (Q|K|V fused: per-row quantization is per
                                      output row, so concatenation is exact)
-        x1  = x + q Wo^T            (residual fused in the GEMM epilogue)
+        a   = attention(rotary(q, k), v)
+        x1  = x + a Wo^T            (residual fused in the GEMM epilogue)
         x   = x1 + proj(act(fc(x1)))
+    With attention=None (the default: the core's linears alone) the O projection
+    reads the query slice of QKV in a's place.
     act = relu^2, or leaky_relu(., 0.5)^2 with act="leaky2"; bits = 5 selects
     the int5 grid (the write-up's MLP_INT5 / ATTN_INT5 configuration).
     """
 
-    def __init__(self, Wq, Wk, Wv, Wo, Wfc, Wproj, bits=6, stream=None, act="relu2"):
+    def __init__(self, Wq, Wk, Wv, Wo, Wfc, Wproj, bits=6, stream=None, act="relu2",
+                 attention=None):
         self.d = Wq.shape[1]
+        self.attention = attention
+        if attention is not None:
+            self.hd = Wq.shape[0] // attention.heads
+            if (Wq.shape[0] != attention.heads * self.hd or Wo.shape[1] != Wq.shape[0] or
+                    Wk.shape[0] != attention.kv_heads * self.hd or Wv.shape[0] != Wk.shape[0]):
+                raise ValueError("projection shapes and head counts disagree")
         self.H = Wfc.shape[0]
         self.bits = bits
         self.act = act
@@ -40,6 +97,10 @@ class RecurrentCore:
             self._buf = (torch.empty((T, self.nqkv), dtype=bf, device=device),
                          torch.empty((T, self.d), dtype=bf, device=device),
                          torch.empty((T, self.H), dtype=bf, device=device))
+            if self.attention is not None:
+                a = self.attention
+                self._att = (torch.empty((T, a.heads * self.hd), dtype=bf, device=device),
+                             torch.empty((a.heads, T), device=device))
         return self._buf
 
     def forward(self, x, R, stream=None, noise=None):
@@ -65,7 +126,13 @@ class RecurrentCore:
             q_qkv, q_o, q_fc, q_proj = ops
             bits = self.bits
             qat.qat_linear_fwd(x, qkv, bits, qw=q_qkv, stream=stream)
-            qat.qat_linear_fwd(qkv, x1, bits, qw=q_o, ldx=self.nqkv, T=T, residual=x, stream=stream)
+            if self.attention is not None:
+                att, lse = self._att
+                self.attention.forward(qkv, att, lse, self.hd, stream)
+                qat.qat_linear_fwd(att, x1, bits, qw=q_o, residual=x, stream=stream)
+            else:
+                qat.qat_linear_fwd(qkv, x1, bits, qw=q_o, ldx=self.nqkv, T=T, residual=x,
+                                   stream=stream)
             qat.qat_mlp_fwd(x1, x, bits, self.d, self.H, qfc=q_fc, qproj=q_proj, residual=x1,
                             h_save=h, stream=stream, act=self.act)
         return x
@@ -91,7 +158,9 @@ class RecurrentCore:
         so that each weight gradient is one GEMM over all R * T token uses:
         states [R+1, T, d] (state 0 is the input, state r+1 the output of
         application r), qkv, x1, pre, h; the gradient's g [R, T, d] (g[r] =
-        dL/d output of application r), dx1, dq [R, T, d], dpre [R, T, H].
+        dL/d output of application r), dx1, dq [R, T, d], dpre [R, T, H]; with
+        attention also its outputs att [R, T, .] and lse [R, heads, T] and the
+        gradient dqkv [R, T, .] (dq then holds the gradient of att).
         They, and the weight gradients dWqkv, dWo, dWfc, dWproj, are allocated
         again when T or R changes: accumulate=True carries gradients across
         calls of the same T and R only."""
@@ -103,8 +172,16 @@ class RecurrentCore:
             self._tb = {"states": e(R + 1, T, d), "qkv": e(R, T, self.nqkv), "x1": e(R, T, d),
                         "pre": e(R, T, H), "h": e(R, T, H), "g": e(R, T, d), "dx1": e(R, T, d),
                         "dq": e(R, T, d), "dpre": e(R, T, H), "dX": e(T, d)}
+            if self.attention is not None:
+                a = self.attention
+                w = a.heads * self.hd
+                self._tb.update(att=e(R, T, w), lse=e(R, a.heads, T, dt=f32), dqkv=e(R, T, self.nqkv),
+                                dq=e(R, T, w))
+                self._attn_ws = torch.empty(
+                    qat.workspace_size(qat.QAT_OP_ATTN_BWD, a.heads, self.hd, T, False),
+                    dtype=torch.uint8, device=device)
             self.dWqkv = e(self.nqkv, d, dt=f32)
-            self.dWo = e(d, d, dt=f32)
+            self.dWo = e(*self.W[1].shape, dt=f32)
             self.dWfc = e(H, d, dt=f32)
             self.dWproj = e(d, H, dt=f32)
             self._tkey = key
@@ -125,8 +202,13 @@ class RecurrentCore:
         for r in range(R):
             q_qkv, q_o, q_fc, q_proj = apps[r]
             qat.qat_linear_fwd(st[r], tb["qkv"][r], self.bits, qw=q_qkv, stream=stream)
-            qat.qat_linear_fwd(tb["qkv"][r], tb["x1"][r], self.bits, qw=q_o, ldx=self.nqkv, T=T,
-                               residual=st[r], stream=stream)
+            if self.attention is not None:
+                self.attention.forward(tb["qkv"][r], tb["att"][r], tb["lse"][r], self.hd, stream)
+                qat.qat_linear_fwd(tb["att"][r], tb["x1"][r], self.bits, qw=q_o, residual=st[r],
+                                   stream=stream)
+            else:
+                qat.qat_linear_fwd(tb["qkv"][r], tb["x1"][r], self.bits, qw=q_o, ldx=self.nqkv, T=T,
+                                   residual=st[r], stream=stream)
             qat.qat_mlp_fwd(tb["x1"][r], st[r + 1], self.bits, self.d, self.H, qfc=q_fc,
                             qproj=q_proj, residual=tb["x1"][r], pre_save=tb["pre"][r],
                             h_save=tb["h"][r], stream=stream, act=self.act)
@@ -136,34 +218,54 @@ class RecurrentCore:
     def _saved(self, r):
         """Application r's kept activations and operands (for backward_application)."""
         tb = self._tb
-        return {"x": tb["states"][r], "qkv": tb["qkv"][r], "x1": tb["x1"][r], "pre": tb["pre"][r],
-                "h": tb["h"][r], "ops": self._apps[r]}
+        s = {"x": tb["states"][r], "qkv": tb["qkv"][r], "x1": tb["x1"][r], "pre": tb["pre"][r],
+             "h": tb["h"][r], "ops": self._apps[r]}
+        if self.attention is not None:
+            s.update(att=tb["att"][r], lse=tb["lse"][r])
+        return s
 
-    def _dx_chain(self, s, g, dx1, dq, dpre, dx, stream):
+    def _dx_chain(self, s, g, dx1, dq, dpre, dx, stream, dqkv=None):
         """The gradient's chain through one application (no weight gradients):
             dpre = (g Wproj) * act'(pre) ; dx1 = g + dpre Wfc   (qat_mlp_bwd)
             dq   = dx1 Wo                                       (qat_linear_bwd)
-            dx   = dx1 + dq Wq                                  (qat_linear_bwd)"""
+            dx   = dx1 + dq Wq                                  (qat_linear_bwd)
+        or, with attention (dq: the gradient of its output),
+            dqkv = attention's and the rotation's backward of dq
+            dx   = dx1 + dqkv Wqkv                              (qat_linear_bwd)"""
         q_qkv, q_o, q_fc, q_proj = s["ops"]
         d = self.d
         qat.qat_mlp_bwd(s["x1"], s["pre"], s["h"], g, self.bits, d, self.H, qfc=q_fc,
                         qproj=q_proj, dX=dx1, dX_residual=g, dpre_save=dpre, stream=stream,
                         act=self.act)
         qat.qat_linear_bwd(None, dx1, self.bits, qw=q_o, dX=dq, stream=stream)
+        if self.attention is not None:
+            self.attention.backward(dq, s["qkv"], s["att"], s["lse"], dqkv, self._attn_ws, self.hd,
+                                    stream)
+            qat.qat_linear_bwd(None, dqkv, self.bits, qw=q_qkv, dX=dx, dX_residual=dx1,
+                               stream=stream)
+            return
         q_q = qat.QWeight(q_qkv.operand[:d], None, None, self.bits)
         qat.qat_linear_bwd(None, dq, self.bits, qw=q_q, dX=dx, dX_residual=dx1, stream=stream)
 
-    def _weight_grads(self, x, qkv, x1, h, g, dx1, dq, dpre, accumulate, stream):
+    def _weight_grads(self, x, qkv, x1, h, g, dx1, dq, dpre, accumulate, stream, att=None,
+                      dqkv=None):
         """The four weight gradients from token-stacked operands (one GEMM each,
         the reduction over every token of every application given):
-            dWproj (+)= g^T h ; dWfc (+)= dpre^T x1 ; dWo (+)= dx1^T q ;
-            dWqkv[:d] (+)= dq^T x ; dWqkv[d:] = 0 unless accumulating
-        (k and v do not reach the output with attention left out)."""
+            dWproj (+)= g^T h ; dWfc (+)= dpre^T x1 ;
+            dWo (+)= dx1^T att ; dWqkv (+)= dqkv^T x
+        or with attention left out (k and v do not reach the output)
+            dWo (+)= dx1^T q ; dWqkv[:d] (+)= dq^T x ; dWqkv[d:] = 0 unless accumulating."""
         d, H = self.d, self.H
         qat.qat_linear_bwd(h, g, self.bits, dW=self.dWproj, N=d, K=H,
                            accumulate_dW=accumulate, stream=stream)
         qat.qat_linear_bwd(x1, dpre, self.bits, dW=self.dWfc, N=H, K=d,
                            accumulate_dW=accumulate, stream=stream)
+        if self.attention is not None:
+            qat.qat_linear_bwd(att, dx1, self.bits, dW=self.dWo, N=d, K=att.shape[1],
+                               accumulate_dW=accumulate, stream=stream)
+            qat.qat_linear_bwd(x, dqkv, self.bits, dW=self.dWqkv, N=self.nqkv, K=d,
+                               accumulate_dW=accumulate, stream=stream)
+            return
         qat.qat_linear_bwd(qkv, dx1, self.bits, dW=self.dWo, N=d, K=d, ldx=self.nqkv,
                            accumulate_dW=accumulate, stream=stream)
         qat.qat_linear_bwd(x, dq, self.bits, dW=self.dWqkv[:d], N=d, K=d,
@@ -182,8 +284,12 @@ class RecurrentCore:
             self._train_buffers(T, 1, g.device)
         tb = self._tb
         dx1, dq, dpre = tb["dx1"][0], tb["dq"][0], tb["dpre"][0]
-        self._dx_chain(s, g, dx1, dq, dpre, dx, stream)
-        self._weight_grads(s["x"], s["qkv"], s["x1"], s["h"], g, dx1, dq, dpre, accumulate, stream)
+        more = {"dqkv": tb["dqkv"][0]} if self.attention is not None else {}
+        self._dx_chain(s, g, dx1, dq, dpre, dx, stream, **more)
+        if self.attention is not None:
+            more["att"] = s["att"]
+        self._weight_grads(s["x"], s["qkv"], s["x1"], s["h"], g, dx1, dq, dpre, accumulate, stream,
+                           **more)
 
     def backward(self, dY, stream=None, accumulate=False):
         """Backward through the applications of the last forward_train, in
@@ -201,12 +307,14 @@ class RecurrentCore:
             tb["g"][R - 1].copy_(dY)
         for r in reversed(range(R)):
             dx = tb["g"][r - 1] if r > 0 else tb["dX"]
+            more = {"dqkv": tb["dqkv"][r]} if self.attention is not None else {}
             self._dx_chain(self._saved(r), tb["g"][r], tb["dx1"][r], tb["dq"][r], tb["dpre"][r],
-                           dx, stream)
+                           dx, stream, **more)
         flat = lambda a: a.reshape(R * T, a.shape[-1])
+        more = {n: flat(tb[n]) for n in ("att", "dqkv")} if self.attention is not None else {}
         self._weight_grads(flat(tb["states"][:R]), flat(tb["qkv"]), flat(tb["x1"]), flat(tb["h"]),
                            flat(tb["g"]), flat(tb["dx1"]), flat(tb["dq"]), flat(tb["dpre"]),
-                           accumulate, stream)
+                           accumulate, stream, **more)
         return tb["dX"]
 
     def flops(self, T, R):
@@ -223,9 +331,12 @@ class HeadMlpStep:
         quantize (every step: the weights change between steps)
         Z = MLP(X); logits = Z Wemb^T
         dZ = dLogits Wemb_q; dWemb = dLogits^T Z; MLP backward -> dX, dWfc, dWproj
+    step() takes dLogits from the caller; step_loss() takes the next words and
+    trains on their mean cross entropy, without ever holding the logits
+    (logits=False then leaves their buffer out).
     """
 
-    def __init__(self, Wemb, Wfc, Wproj, T, head_bits=8, mlp_bits=6, act="relu2"):
+    def __init__(self, Wemb, Wfc, Wproj, T, head_bits=8, mlp_bits=6, act="relu2", logits=True):
         dev = Wemb.device
         self.W = (Wemb, Wfc, Wproj)
         self.vocab, self.d = Wemb.shape
@@ -238,7 +349,9 @@ class HeadMlpStep:
         self.q = [qat.QWeight(e(*w.shape), e(w.shape[0], dt=torch.float32), None, b)
                   for w, b in ((Wemb, head_bits), (Wfc, mlp_bits), (Wproj, mlp_bits))]
         self.pre, self.h = e(T, self.H), e(T, self.H)
-        self.Z, self.logits, self.dZ, self.dX = e(T, self.d), e(T, self.vocab), e(T, self.d), e(T, self.d)
+        self.Z, self.dZ, self.dX = e(T, self.d), e(T, self.d), e(T, self.d)
+        self.logits = e(T, self.vocab) if logits else None
+        self._loss = None
         self.dWemb = e(self.vocab, self.d, dt=torch.float32)
         self.dWfc = e(self.H, self.d, dt=torch.float32)
         self.dWproj = e(self.d, self.H, dt=torch.float32)
@@ -272,6 +385,45 @@ class HeadMlpStep:
         self.quantize(stream)
         self.forward(X, stream)
         self.backward(X, dLogits, stream, on_head_grad)
+
+    def _loss_buffers(self):
+        """loss and log-sum-exp per token, (mean loss, 1 / counted tokens), workspace."""
+        if self._loss is None:
+            dev = self.W[0].device
+            n = qat.workspace_size(qat.QAT_OP_CE_BWD, self.vocab, self.d, self.T, False)
+            self._loss = (torch.empty(self.T, device=dev), torch.empty(self.T, device=dev),
+                          torch.empty(2, device=dev), torch.empty(n, dtype=torch.uint8, device=dev))
+        return self._loss
+
+    def forward_loss(self, X, targets, stream=None):
+        """Mean cross entropy of targets [T] int64 (outside [0, vocab): not counted),
+        a device scalar; the losses per token are in self.loss."""
+        qe, qf, qp = self.q
+        self.loss, lse, mean, ws = self._loss_buffers()
+        qat.qat_mlp_fwd(X, self.Z, self.mlp_bits, self.d, self.H, qfc=qf, qproj=qp,
+                        pre_save=self.pre, h_save=self.h, stream=stream, act=self.act)
+        qat.qat_ce_fwd(self.Z, targets, self.loss, lse, self.head_bits, qw=qe, mean=mean,
+                       workspace=ws, stream=stream)
+        return mean[0]
+
+    def backward_loss(self, X, targets, stream=None, on_head_grad=None):
+        """Gradients of the mean loss of the last forward_loss."""
+        qe, qf, qp = self.q
+        _, lse, mean, ws = self._loss_buffers()
+        qat.qat_ce_bwd(self.Z, targets, lse, self.head_bits, qw=qe, gscale=mean[1:], dZ=self.dZ,
+                       dW=self.dWemb, workspace=ws, stream=stream)
+        if on_head_grad is not None:
+            on_head_grad()
+        qat.qat_mlp_bwd(X, self.pre, self.h, self.dZ, self.mlp_bits, self.d, self.H, qfc=qf,
+                        qproj=qp, dX=self.dX, dWfc=self.dWfc, dWproj=self.dWproj,
+                        workspace=self.ws, stream=stream, act=self.act)
+
+    def step_loss(self, X, targets, stream=None, on_head_grad=None):
+        """Quantize, forward, loss, backward: returns the mean loss (a device scalar)."""
+        self.quantize(stream)
+        mean = self.forward_loss(X, targets, stream)
+        self.backward_loss(X, targets, stream, on_head_grad)
+        return mean
 
     def grads(self):
         return [self.dWemb, self.dWfc, self.dWproj]
