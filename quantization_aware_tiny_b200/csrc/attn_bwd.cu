@@ -11,10 +11,11 @@
 // sum ever leaves a CTA: no fp32 copy of dQ in memory, no atomics, and the same
 // inputs give the same bits.
 //
-// P and dS are rounded to bf16 for the second products.  In both kernels they
-// replace S and dP in tensor memory and are read from there as operand A; the
-// keys go in blocks of 64 (dq) and the queries too (dkv), so that two blocks are
-// in flight: the tensor core works on one while the other is turned into dS.
+// P and dS are rounded to bf16 for the second products.  They go back to tensor
+// memory and are read from there as operand A.  Both kernels form P as soon as S
+// is there and dS once dP is, so that the products of the next block (and the
+// sums of this one) run below the exponentials; four math warpgroups share a
+// block, 32 of its 128 columns each.
 #include <algorithm>
 #include <atomic>
 
@@ -25,27 +26,88 @@ namespace qat {
 
 namespace {
 
-constexpr int BT = 128;  // rows of a stationary tile
-constexpr int BS = 64;   // rows of a streamed block
+constexpr int BT = 128;  // rows of the stationary tile and of a streamed block
 
 template <int NC>
 struct Cfg {
-  static constexpr int THREADS = 384;
-  // registers per thread: 168 at launch, 72 + 216 + 216 = 3 * 168 after the split
-  static constexpr int REGS_ISSUE = 72, REGS_MATH = 216;
-  static constexpr int TILE = tile_bytes(BT, NC), BLOCK = tile_bytes(BS, NC);
-  static constexpr int DQ_ST = NC == 1 ? 4 : 3;   // stages (K and V block each)
-  static constexpr int DQ_SMEM = 4 * TILE + DQ_ST * 2 * BLOCK + 1024 + 256;
-  static constexpr int KV_ST = 4;                 // stages (Q and dO block each)
-  static constexpr int ROWS_BYTES = 8 * 2 * BS * 4;  // lse and delta of a block, per warp
-  static constexpr int KV_SMEM = 2 * TILE + KV_ST * 2 * BLOCK + ROWS_BYTES + 1024 + 256;
-  static constexpr int COLS = 64 * NC;            // tensor-memory columns of an accumulator
+  // 16 math warps, four to a scheduler: with 8 (64 columns per thread) the waits for
+  // tensor memory and for the exponentials lay bare, 3,700 cycles a block instead of
+  // about 2,000 (dq, head size 64)
+  static constexpr int GROUPS = 4;                  // math warpgroups
+  static constexpr int MC = BT / GROUPS;            // columns of a block per thread
+  static constexpr int THREADS = 128 * (1 + GROUPS);
+  // registers per thread: 96 at launch (65,536 / 640), 56 + 4 * 104 <= 5 * 96 after the split
+  static constexpr int REGS_ISSUE = 56, REGS_MATH = 104;
+  static constexpr int TILE = tile_bytes(BT, NC);
+  static constexpr int ST = NC == 1 ? 4 : 2;        // stages of either ring
+  static constexpr int ROWS_BYTES = 4 * GROUPS * 2 * MC * 4;  // dkv: lse and delta, per warp
+  static constexpr int SMEM = (2 + 2 * ST) * TILE + ROWS_BYTES + 1024 + 256;
+  static constexpr int COLS = 64 * NC;              // tensor-memory columns of an accumulator
 };
 
-// bf16(a * f) of one accumulator row of hd columns, from tensor memory to global.
+// The rings and barriers of both kernels: two stationary tiles, two rings.
+template <int NC>
+struct Smem {
+  using C = Cfg<NC>;
+  uint8_t *fix_a, *fix_b, *ring_a, *ring_b;
+  float* rows;
+  uint64_t *fix_full, *a_full, *a_empty, *b_full, *b_empty;
+  uint64_t *s_full, *dp_full, *p_full, *ds_full, *acc_full, *mma_done;
+  uint32_t* tmem_slot;
+  volatile int* abort_flag;
+
+  __device__ explicit Smem(uint8_t* raw) {
+    fix_a = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    fix_b = fix_a + C::TILE;
+    ring_a = fix_b + C::TILE;
+    ring_b = ring_a + C::ST * C::TILE;
+    rows = reinterpret_cast<float*>(ring_b + C::ST * C::TILE);
+    fix_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(rows) + C::ROWS_BYTES);
+    a_full = fix_full + 1;
+    a_empty = a_full + C::ST;
+    b_full = a_empty + C::ST;
+    b_empty = b_full + C::ST;
+    s_full = b_empty + C::ST;
+    dp_full = s_full + 1;
+    p_full = dp_full + 1;
+    ds_full = p_full + 1;
+    acc_full = ds_full + 1;
+    mma_done = acc_full + 1;
+    tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert((1 + 4 * C::ST + 6) * 8 + 8 <= 256, "barrier block overflow");
+  }
+  __device__ void init() {
+    mbar_init(fix_full, 1);
+    for (int i = 0; i < C::ST; ++i) {
+      mbar_init(&a_full[i], 1);
+      mbar_init(&a_empty[i], 1);
+      mbar_init(&b_full[i], 1);
+      mbar_init(&b_empty[i], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_full, 4 * C::GROUPS);  // the math warps
+    mbar_init(ds_full, 4 * C::GROUPS);
+    mbar_init(acc_full, 1);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+};
+
+// One staged tile of `head`, rows from `row` on.
+template <int NC>
+__device__ __forceinline__ void load_tile(const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int head, int row) {
+#pragma unroll
+  for (int c = 0; c < NC; ++c) tma_load_3d(map, bar, dst + c * BT * 128, c * 64, head, row);
+}
+
+// bf16(a * f) of one accumulator row of hd columns, from tensor memory to global:
+// its 32-column pieces from, from + step, ...
 __device__ __forceinline__ void store_row(__nv_bfloat16* out, uint32_t t, int hd, float f, bool any,
-                                          bool write) {
-  for (int c = 0; c < (hd + 31) / 32; ++c) {
+                                          bool write, int from, int step) {
+  for (int c = from; c < (hd + 31) / 32; c += step) {
     uint32_t o[32];
     if (any) {
       tmem_ld32(t + c * 32, o);
@@ -66,173 +128,142 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* out, uint32_t t, int hd
 
 // ------------------------------------------------------------------------ dQ
 
+// A CTA owns 128 queries of a head.  Tensor memory: S, dP (128 columns each), dS
+// (bf16, 64), dQ.  Issue order: S(n + 1) once S(n) is read; then, once dS(n) is
+// written, dQ += dS(n) K(n) and dP(n + 1) -- whose arrival thus also says that
+// dS(n) has been read.
 template <int NC>
 __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     attn_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const AttnArgs p) {
   using C = Cfg<NC>;
-  constexpr int ST = C::DQ_ST;
+  constexpr int ST = C::ST;
+  constexpr uint32_t T_DP = BT, T_DS = 2 * BT, T_DQ = 2 * BT + BT / 2;
+  static_assert(T_DQ + C::COLS <= 512, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint8_t* sQ = smem;
-  uint8_t* sdO = sQ + 2 * C::TILE;
-  uint8_t* sKV = sdO + 2 * C::TILE;  // stage: K block, V block
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + ST * 2 * C::BLOCK);
-  uint64_t* q_full = bars;
-  uint64_t* kv_full = q_full + 1;
-  uint64_t* kv_empty = kv_full + ST;
-  uint64_t* s_full = kv_empty + ST;  // [2] S and dP of a tile are in tensor memory
-  uint64_t* ds_full = s_full + 2;    // [2] dS of a tile is
-  uint64_t* acc_full = ds_full + 2;  // [2] dQ of a tile is complete
-  uint64_t* mma_done = acc_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((1 + 2 * ST + 7) * 8 + 8 <= 256, "barrier block overflow");
-  constexpr uint32_t PER_TILE = 2 * BS + C::COLS;  // tensor memory of a tile: S, dP, dQ
-  static_assert(2 * PER_TILE <= 512, "tensor memory");
+  const Smem<NC> m(smem_raw);  // fixed: Q, dO; rings: K, V
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int head = static_cast<int>(blockIdx.x % p.heads);
   const Seq sq = seq_of(p, static_cast<int>(blockIdx.x / p.heads));
-  const int i0 = static_cast<int>(gridDim.y - 1 - blockIdx.y) * 2 * BT;  // longest rows first
+  const int i0 = static_cast<int>(gridDim.y - 1 - blockIdx.y) * BT;  // longest rows first
   if (i0 >= sq.nq) return;
-  int b0[2], b1[2], j0, j1;
-  key_blocks<BT, BS>(p, sq, i0, b0, b1, j0, j1);
+  int j0, j1;
+  key_blocks<BT, BT>(p, sq, i0, j0, j1);
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&ds_full[i], 4);
-      mbar_init(&acc_full[i], 1);
-    }
-    mbar_init(mma_done, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
+    Smem<NC>(smem_raw).init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmdO);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(m.tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *m.tmem_slot;
   const int kv_head = head / p.group;
+  const int steps = j1 - j0;
 
   if (warp < 4) {
     set_regs_dec<C::REGS_ISSUE>();
-    if (warp == 0 && lane == 0 && j1 > j0) {
+    if (warp == 0 && lane == 0 && steps > 0) {
       // ------------------------------------------------ TMA producer
-      const int tiles = i0 + BT < sq.nq ? 2 : 1;
-      mbar_arrive_expect_tx(q_full, 2 * tiles * C::TILE);
-      for (int w = 0; w < tiles; ++w)
-        for (int c = 0; c < NC; ++c) {
-          const int at = w * C::TILE + c * BT * 128, row = static_cast<int>(sq.q0) + i0 + w * BT;
-          tma_load_3d(&tmQ, q_full, sQ + at, c * 64, head, row);
-          tma_load_3d(&tmdO, q_full, sdO + at, c * 64, head, row);
-        }
-      int issued = 0;
-      for (int j = j0; j < j1; ++j, ++issued) {
-        const int st = issued % ST;
-        if (!mbar_wait(&kv_empty[st], ((issued / ST) & 1) ^ 1, abort_flag, p.err)) break;
-        mbar_arrive_expect_tx(&kv_full[st], 2 * C::BLOCK);
-        const int row = static_cast<int>(sq.k0) + j * BS;
-        for (int c = 0; c < NC; ++c) {
-          uint8_t* dst = sKV + st * 2 * C::BLOCK + c * BS * 128;
-          tma_load_3d(&tmK, &kv_full[st], dst, c * 64, kv_head, row);
-          tma_load_3d(&tmV, &kv_full[st], dst + C::BLOCK, c * 64, kv_head, row);
-        }
+      const int row = static_cast<int>(sq.q0) + i0;
+      mbar_arrive_expect_tx(m.fix_full, 2 * C::TILE);
+      load_tile<NC>(&tmQ, m.fix_full, m.fix_a, head, row);
+      load_tile<NC>(&tmdO, m.fix_full, m.fix_b, head, row);
+      int na = 0, nb = 0;
+      for (int n = 0; n < steps; ++n) {
+        const int st = n % ST, krow = static_cast<int>(sq.k0) + (j0 + n) * BT;
+        const uint32_t free = ((n / ST) & 1) ^ 1;
+        if (!mbar_wait(&m.a_empty[st], free, m.abort_flag, p.err)) break;
+        mbar_arrive_expect_tx(&m.a_full[st], C::TILE);
+        load_tile<NC>(&tmK, &m.a_full[st], m.ring_a + st * C::TILE, kv_head, krow);
+        ++na;
+        if (!mbar_wait(&m.b_empty[st], free, m.abort_flag, p.err)) break;
+        mbar_arrive_expect_tx(&m.b_full[st], C::TILE);
+        load_tile<NC>(&tmV, &m.b_full[st], m.ring_b + st * C::TILE, kv_head, krow);
+        ++nb;
       }
       // every copy has landed before the block may exit (at once, unless a wait ran out)
-      mbar_drain(q_full, 0);
-      for (int n = max(0, issued - ST); n < issued; ++n) mbar_drain(&kv_full[n % ST], (n / ST) & 1);
-    } else if (warp == 1 && j1 > j0) {
+      mbar_drain(m.fix_full, 0);
+      for (int n = max(0, na - ST); n < na; ++n) mbar_drain(&m.a_full[n % ST], (n / ST) & 1);
+      for (int n = max(0, nb - ST); n < nb; ++n) mbar_drain(&m.b_full[n % ST], (n / ST) & 1);
+    } else if (warp == 1 && steps > 0) {
       // ------------------------------------------------ MMA issuer
       const int ks = (p.hd + 15) / 16;
-      const uint32_t id_s = idesc_bf16(BT, BS, false, false);
+      const uint32_t id_s = idesc_bf16(BT, BT, false, false);
       const uint32_t id_q = idesc_bf16(BT, ks * 16, false, true);
-      bool ok = warp_wait(q_full, 0, abort_flag, p.err);
-      uint32_t dph[2] = {0, 0};
-      for (int j = j0; ok && j <= j1; ++j) {
-        const int n = j - j0, st = n % ST, pst = (n + ST - 1) % ST;
-        uint8_t* kb = sKV + st * 2 * C::BLOCK;
-        if (j < j1) {
-          ok = warp_wait(&kv_full[st], (n / ST) & 1, abort_flag, p.err);
-          if (!ok) break;
-          const int rows = sq.nk - j * BS;
-          if (rows < BS) {
-            clear_rows<NC>(kb, BS, rows, lane);
-            clear_rows<NC>(kb + C::BLOCK, BS, rows, lane);
-          }
+      const uint32_t issue = elect_lane();
+      const uint64_t fix_a = kmajor_desc<BT>(m.fix_a), fix_b = kmajor_desc<BT>(m.fix_b);
+      const uint64_t ring_a = kmajor_desc<BT>(m.ring_a), ring_b = kmajor_desc<BT>(m.ring_b);
+      const uint64_t rows_a = rows_desc<BT>(m.ring_a);
+      constexpr uint32_t STAGE = C::TILE >> 4;
+      bool ok = warp_wait(m.fix_full, 0, m.abort_flag, p.err);
+      auto scores = [&](int n) {  // S = Q K^T of block n
+        ok = ok && warp_wait(&m.a_full[n % ST], (n / ST) & 1, m.abort_flag, p.err);
+        if (!ok) return;
+        const int live = sq.nk - (j0 + n) * BT;
+        if (live < BT) clear_rows<NC>(m.ring_a + n % ST * C::TILE, BT, live, lane);
+        tc_fence_after();
+        product<NC, BT>(tmem, fix_a, ring_a + n % ST * STAGE, id_s, ks, issue);
+        mma_commit(m.s_full, issue);
+      };
+      auto dprobs = [&](int n) {  // dP = dO V^T of block n
+        ok = ok && warp_wait(&m.b_full[n % ST], (n / ST) & 1, m.abort_flag, p.err);
+        if (!ok) return;
+        const int live = sq.nk - (j0 + n) * BT;
+        if (live < BT) clear_rows<NC>(m.ring_b + n % ST * C::TILE, BT, live, lane);
+        tc_fence_after();
+        product<NC, BT>(tmem + T_DP, fix_b, ring_b + n % ST * STAGE, id_s, ks, issue);
+        mma_commit(m.dp_full, issue);
+        mma_commit(&m.b_empty[n % ST], issue);
+      };
+      scores(0);
+      dprobs(0);
+      for (int n = 0; ok && n < steps; ++n) {
+        if (n + 1 < steps) {
+          ok = warp_wait(m.p_full, n & 1, m.abort_flag, p.err);  // S(n) has been read
+          scores(n + 1);
         }
+        ok = ok && warp_wait(m.ds_full, n & 1, m.abort_flag, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t k = rows_a + n % ST * STAGE;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const uint32_t t = tmem + w * PER_TILE;
-          if (j > j0 && j - 1 >= b0[w] && j - 1 < b1[w]) {  // dQ += dS K of block j - 1
-            ok = warp_wait(&ds_full[w], dph[w], abort_flag, p.err);
-            dph[w] ^= 1u;
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-              const uint32_t more = j - 1 > b0[w];
-#pragma unroll
-              for (int kk = 0; kk < BS / 16; ++kk)
-                umma_bf16_ts(t + 2 * BS, t + kk * 8, rows_desc(sKV + pst * 2 * C::BLOCK, BS, kk), id_q,
-                             (kk > 0) | more);
-              if (j == b1[w]) umma_commit(&acc_full[w]);
-            }
-          }
-          if (j < j1 && j >= b0[w] && j < b1[w]) {  // S = Q K^T, dP = dO V^T of block j
-            tc_fence_after();
-            if (lane == 0) {
-              for (int kk = 0; kk < ks; ++kk)
-                umma_bf16(t, kmajor_desc(sQ + w * C::TILE, BT, kk), kmajor_desc(kb, BS, kk), id_s, kk > 0);
-              for (int kk = 0; kk < ks; ++kk)
-                umma_bf16(t + BS, kmajor_desc(sdO + w * C::TILE, BT, kk),
-                          kmajor_desc(kb + C::BLOCK, BS, kk), id_s, kk > 0);
-              umma_commit(&s_full[w]);
-            }
-          }
-        }
-        if (ok && j > j0 && lane == 0) umma_commit(&kv_empty[pst]);
+        for (int kk = 0; kk < BT / 16; ++kk)
+          mma_ts(tmem + T_DQ, tmem + T_DS + kk * 8, k + rows_step(kk), id_q, (kk > 0) | (n > 0), issue);
+        mma_commit(&m.a_empty[n % ST], issue);
+        if (n + 1 == steps) mma_commit(m.acc_full, issue);
+        if (n + 1 < steps) dprobs(n + 1);
       }
-      if (lane == 0) umma_commit(mma_done);
-      warp_wait(mma_done, 0, abort_flag, p.err);  // before tensor memory is freed
+      mma_commit(m.mma_done, issue);
+      warp_wait(m.mma_done, 0, m.abort_flag, p.err);  // before tensor memory is freed
     }
   } else {
     set_regs_inc<C::REGS_MATH>();
-    // ------------------------------------------------ dS, a query row per thread
+    // ------------------------------------------------ dS: a thread holds 32 keys of a query row
     const int w = (warp - 4) >> 2;
-    const int quarter = warp & 3;
-    const int first = i0 + w * BT;
-    const int i = first + quarter * 32 + lane;
-    const uint32_t t = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + w * PER_TILE;
+    const int quarter = warp & 3;  // tensor-memory lanes this warp may access
+    const int i = i0 + quarter * 32 + lane;
+    const uint32_t t = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float c2 = p.scale * kAttnLog2e;
     const int64_t at = sq.q0 + i;
     int lo, hi;
     keys_of(p, sq, i, lo, hi);
-    int full0 = 0, full1 = 0;  // keys that every row of the tile sees
-    if (first < sq.nq) {
-      int a, b;
-      keys_of(p, sq, first, a, b);
-      full1 = b;
-      keys_of(p, sq, first + BT - 1, a, b);
-      full0 = a;
-    }
+    int full0, full1, unused;  // keys that every row of the tile sees
+    keys_of(p, sq, i0, unused, full1);
+    keys_of(p, sq, i0 + BT - 1, full0, unused);
     float lse2 = 0.0f, delta = 0.0f;
     if (i < sq.nq) {
-      lse2 = p.lse[head * p.Tq + at] * kAttnLog2e;
+      const float l = p.lse[head * p.Tq + at];
+      lse2 = l == -INFINITY ? 0.0f : l * kAttnLog2e;  // (no key: every place is masked below)
       const uint4* o = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.O) + at * p.ldo + head * p.hd);
       const uint4* d = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dO) + at * p.lddo + head * p.hd);
       float part[2] = {0.0f, 0.0f};
@@ -249,52 +280,55 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
         }
       }
       delta = part[0] + part[1];
-      p.delta[head * p.Tq + at] = delta;  // for the other kernel
+      if (w == 0) p.delta[head * p.Tq + at] = delta;  // for the other kernel
     }
-    uint32_t ph = 0;
+    const float2 cc = make_float2(c2, c2), nl = make_float2(-lse2, -lse2), nd = make_float2(-delta, -delta);
+    const uint32_t count = static_cast<uint32_t>(hi - lo);
     bool ok = true;
-    for (int j = b0[w]; j < b1[w]; ++j) {
-      if (!warp_wait(&s_full[w], ph, abort_flag, p.err)) { ok = false; break; }
-      ph ^= 1u;
+    for (int n = 0; n < steps; ++n) {
+      if (!warp_wait(m.s_full, n & 1, m.abort_flag, p.err)) { ok = false; break; }
       tc_fence_after();
-      uint32_t s[2][32], g[2][32];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        tmem_ld32(t + c * 32, s[c]);
-        tmem_ld32(t + BS + c * 32, g[c]);
-      }
+      uint32_t s[32];
+      tmem_ld32(t + w * 32, s);
       tmem_ld_wait();
-      const int key0 = j * BS;
-      const bool masked = key0 < full0 || key0 + BS > full1;
-      uint32_t pk[32];
-      const float2 cc = make_float2(c2, c2), nl = make_float2(-lse2, -lse2), nd = make_float2(-delta, -delta);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(m.p_full);
+      const int key0 = (j0 + n) * BT;
+      if (key0 < full0 || key0 + BT > full1) {
+        const int a = lo - key0 - w * 32;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+        for (int k = 0; k < 32; ++k)
+          if (static_cast<uint32_t>(k - a) >= count) s[k] = 0xff800000u;  // -inf
+      }
+      float2 pr[16];
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          const float2 x = fma2(make_float2(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), cc, nl);
-          const float2 y = add2(make_float2(__uint_as_float(g[c][k]), __uint_as_float(g[c][k + 1])), nd);
-          float2 ds = mul2(make_float2(attn_exp2(x.x), attn_exp2(x.y)), y);
-          if (masked) {
-            const uint32_t n = static_cast<uint32_t>(hi - lo);
-            const int a = key0 + c * 32 + k - lo;
-            if (static_cast<uint32_t>(a) >= n) ds.x = 0.0f;
-            if (static_cast<uint32_t>(a + 1) >= n) ds.y = 0.0f;
-          }
-          pk[c * 16 + k / 2] = pack2(ds.x, ds.y);
-        }
-      tmem_st32(t, pk);
+      for (int k = 0; k < 16; ++k) {
+        const float2 x = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), cc, nl);
+        pr[k] = make_float2(attn_exp2(x.x), attn_exp2(x.y));
+      }
+      if (!warp_wait(m.dp_full, n & 1, m.abort_flag, p.err)) { ok = false; break; }
+      tc_fence_after();
+      tmem_ld32(t + T_DP + w * 32, s);
+      tmem_ld_wait();
+      uint32_t pk[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float2 y = add2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), nd);
+        const float2 ds = mul2(pr[k], y);
+        pk[k] = pack2(ds.x, ds.y);
+      }
+      tmem_st16(t + T_DS + w * 16, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ds_full[w]);
+      if (lane == 0) mbar_arrive(m.ds_full);
     }
-    const bool any = b1[w] > b0[w];
-    if (ok && any) ok = warp_wait(&acc_full[w], 0, abort_flag, p.err);
+    if (ok && steps > 0) ok = warp_wait(m.acc_full, 0, m.abort_flag, p.err);
     tc_fence_after();
-    if (ok && first < sq.nq)
-      store_row(static_cast<__nv_bfloat16*>(p.dQ) + at * p.lddq + head * p.hd, t + 2 * BS, p.hd, p.scale,
-                any, i < sq.nq);
+    if (ok)  // the warpgroups store a quarter of the row each
+      store_row(static_cast<__nv_bfloat16*>(p.dQ) + at * p.lddq + head * p.hd, t + T_DQ, p.hd, p.scale,
+                steps > 0, i < sq.nq, w, C::GROUPS);
     tc_fence_before();
   }
   __syncthreads();
@@ -306,230 +340,217 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
 
 // -------------------------------------------------------------------- dK, dV
 
+// A CTA owns 128 keys of a key head.  Tensor memory: S^T and dP^T (128 columns
+// each; P^T and dS^T replace them as bf16, each warpgroup within the columns it
+// reads), dV, dK.  Issue order: dV += P^T(n) dO(n) and S^T(n + 1) once P(n) is
+// written, dK += dS^T(n) Q(n) and dP^T(n + 1) once dS(n) is.
 template <int NC>
 __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     attn_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const AttnArgs p) {
   using C = Cfg<NC>;
-  constexpr int ST = C::KV_ST;
+  constexpr int ST = C::ST;
+  constexpr uint32_t T_DP = BT, T_DV = 2 * BT, T_DK = 2 * BT + C::COLS;
+  static_assert(T_DK + C::COLS <= 512, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint8_t* sK = smem;
-  uint8_t* sV = sK + C::TILE;
-  uint8_t* sQ = sV + C::TILE;  // stage: Q block, dO block
-  float* rows = reinterpret_cast<float*>(sQ + ST * 2 * C::BLOCK);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(rows) + C::ROWS_BYTES);
-  uint64_t* k_full = bars;
-  uint64_t* q_full = k_full + 1;
-  uint64_t* q_empty = q_full + ST;
-  uint64_t* s_full = q_empty + ST;  // [2] S^T and dP^T of a buffer are in tensor memory
-  uint64_t* ds_full = s_full + 2;   // [2] P^T and dS^T of a buffer are
-  uint64_t* acc_full = ds_full + 2;
-  uint64_t* mma_done = acc_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((1 + 2 * ST + 6) * 8 + 8 <= 256, "barrier block overflow");
-  constexpr uint32_t ACC = 4 * BS;  // dV, then dK, behind two buffers of S^T and dP^T
-  static_assert(ACC + 2 * C::COLS <= 512, "tensor memory");
+  const Smem<NC> m(smem_raw);  // fixed: K, V; rings: Q, dO
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int kv_heads = p.heads / p.group;
   const int kv_head = static_cast<int>(blockIdx.x % kv_heads);
   const Seq sq = seq_of(p, static_cast<int>(blockIdx.x / kv_heads));
   const int key0 = static_cast<int>(blockIdx.y) * BT;  // early keys are seen by most queries: first
   if (key0 >= sq.nk) return;
-  // Queries that see some key of this tile, and their blocks.
-  int qa, qb, ra, rb;
-  queries_of(p, sq, key0, qa, rb);
-  queries_of(p, sq, min(key0 + BT, sq.nk) - 1, ra, qb);
-  const int j0 = qa / BS, nb = qb > qa ? (qb + BS - 1) / BS - j0 : 0;
+  // Queries [qa, qb) see some key of this tile, [full0, full1) every key of it.
+  int qa, qb, full0, full1;
+  queries_of(p, sq, key0, qa, full1);
+  queries_of(p, sq, min(key0 + BT, sq.nk) - 1, full0, qb);
+  const int j0 = qa / BT, nb = qb > qa ? (qb + BT - 1) / BT - j0 : 0;
   const int steps = nb * p.group;  // step n: head n / nb of the group, block j0 + n % nb
 
   if (threadIdx.x == 0) {
-    mbar_init(k_full, 1);
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&ds_full[i], 4);
-    }
-    mbar_init(acc_full, 1);
-    mbar_init(mma_done, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
+    Smem<NC>(smem_raw).init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmdO);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(m.tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *m.tmem_slot;
 
   if (warp < 4) {
     set_regs_dec<C::REGS_ISSUE>();
     if (warp == 0 && lane == 0 && steps > 0) {
       // ------------------------------------------------ TMA producer
-      mbar_arrive_expect_tx(k_full, 2 * C::TILE);
-      for (int c = 0; c < NC; ++c) {
-        const int row = static_cast<int>(sq.k0) + key0;
-        tma_load_3d(&tmK, k_full, sK + c * BT * 128, c * 64, kv_head, row);
-        tma_load_3d(&tmV, k_full, sV + c * BT * 128, c * 64, kv_head, row);
+      const int krow = static_cast<int>(sq.k0) + key0;
+      mbar_arrive_expect_tx(m.fix_full, 2 * C::TILE);
+      load_tile<NC>(&tmK, m.fix_full, m.fix_a, kv_head, krow);
+      load_tile<NC>(&tmV, m.fix_full, m.fix_b, kv_head, krow);
+      int na = 0, nb_ = 0;
+      for (int n = 0; n < steps; ++n) {
+        const int st = n % ST, head = kv_head * p.group + n / nb;
+        const int row = static_cast<int>(sq.q0) + (j0 + n % nb) * BT;
+        const uint32_t free = ((n / ST) & 1) ^ 1;
+        if (!mbar_wait(&m.a_empty[st], free, m.abort_flag, p.err)) break;
+        mbar_arrive_expect_tx(&m.a_full[st], C::TILE);
+        load_tile<NC>(&tmQ, &m.a_full[st], m.ring_a + st * C::TILE, head, row);
+        ++na;
+        if (!mbar_wait(&m.b_empty[st], free, m.abort_flag, p.err)) break;
+        mbar_arrive_expect_tx(&m.b_full[st], C::TILE);
+        load_tile<NC>(&tmdO, &m.b_full[st], m.ring_b + st * C::TILE, head, row);
+        ++nb_;
       }
-      int n = 0;
-      for (; n < steps; ++n) {
-        const int st = n % ST;
-        if (!mbar_wait(&q_empty[st], ((n / ST) & 1) ^ 1, abort_flag, p.err)) break;
-        mbar_arrive_expect_tx(&q_full[st], 2 * C::BLOCK);
-        const int head = kv_head * p.group + n / nb;
-        const int row = static_cast<int>(sq.q0) + (j0 + n % nb) * BS;
-        for (int c = 0; c < NC; ++c) {
-          uint8_t* dst = sQ + st * 2 * C::BLOCK + c * BS * 128;
-          tma_load_3d(&tmQ, &q_full[st], dst, c * 64, head, row);
-          tma_load_3d(&tmdO, &q_full[st], dst + C::BLOCK, c * 64, head, row);
-        }
-      }
-      mbar_drain(k_full, 0);
-      for (int m = max(0, n - ST); m < n; ++m) mbar_drain(&q_full[m % ST], (m / ST) & 1);
+      mbar_drain(m.fix_full, 0);
+      for (int n = max(0, na - ST); n < na; ++n) mbar_drain(&m.a_full[n % ST], (n / ST) & 1);
+      for (int n = max(0, nb_ - ST); n < nb_; ++n) mbar_drain(&m.b_full[n % ST], (n / ST) & 1);
     } else if (warp == 1 && steps > 0) {
       // ------------------------------------------------ MMA issuer
       const int ks = (p.hd + 15) / 16;
-      const uint32_t id_s = idesc_bf16(BT, BS, false, false);
+      const uint32_t id_s = idesc_bf16(BT, BT, false, false);
       const uint32_t id_a = idesc_bf16(BT, ks * 16, false, true);
-      bool ok = warp_wait(k_full, 0, abort_flag, p.err);
-      for (int n = 0; ok && n <= steps; ++n) {
-        if (n < steps) {  // S^T = K Q^T, dP^T = V dO^T of step n
-          const int st = n % ST;
-          ok = warp_wait(&q_full[st], (n / ST) & 1, abort_flag, p.err);
-          if (!ok) break;
-          uint8_t* q = sQ + st * 2 * C::BLOCK;
-          const int live = sq.nq - (j0 + n % nb) * BS;
-          if (live < BS) {
-            clear_rows<NC>(q, BS, live, lane);
-            clear_rows<NC>(q + C::BLOCK, BS, live, lane);
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t t = tmem + (n & 1) * 2 * BS;
-            for (int kk = 0; kk < ks; ++kk)
-              umma_bf16(t, kmajor_desc(sK, BT, kk), kmajor_desc(q, BS, kk), id_s, kk > 0);
-            for (int kk = 0; kk < ks; ++kk)
-              umma_bf16(t + BS, kmajor_desc(sV, BT, kk), kmajor_desc(q + C::BLOCK, BS, kk), id_s, kk > 0);
-            umma_commit(&s_full[n & 1]);
-          }
-        }
-        if (n > 0) {  // dV += P^T dO, dK += dS^T Q of step n - 1
-          const int m = n - 1, st = m % ST;
-          ok = warp_wait(&ds_full[m & 1], (m >> 1) & 1, abort_flag, p.err);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint8_t* q = sQ + st * 2 * C::BLOCK;
-            const uint32_t t = tmem + (m & 1) * 2 * BS;
+      const uint32_t issue = elect_lane();
+      const uint64_t fix_a = kmajor_desc<BT>(m.fix_a), fix_b = kmajor_desc<BT>(m.fix_b);
+      const uint64_t ring_a = kmajor_desc<BT>(m.ring_a), ring_b = kmajor_desc<BT>(m.ring_b);
+      const uint64_t rows_a = rows_desc<BT>(m.ring_a), rows_b = rows_desc<BT>(m.ring_b);
+      constexpr uint32_t STAGE = C::TILE >> 4;
+      bool ok = warp_wait(m.fix_full, 0, m.abort_flag, p.err);
+      // X^T = fixed streamed^T of step n
+      auto scores = [&](int n, uint64_t* full, uint8_t* ring, uint64_t b, uint64_t fix, uint32_t t, uint64_t* done) {
+        ok = ok && warp_wait(&full[n % ST], (n / ST) & 1, m.abort_flag, p.err);
+        if (!ok) return;
+        const int live = sq.nq - (j0 + n % nb) * BT;
+        if (live < BT) clear_rows<NC>(ring + n % ST * C::TILE, BT, live, lane);
+        tc_fence_after();
+        product<NC, BT>(tmem + t, fix, b + n % ST * STAGE, id_s, ks, issue);
+        mma_commit(done, issue);
+      };
+      // accumulator += (bf16 probabilities at t) . streamed rows of step n
+      auto add = [&](int n, uint64_t* ready, uint32_t t, uint32_t acc, uint64_t rows, uint64_t* empty) {
+        ok = ok && warp_wait(ready, n & 1, m.abort_flag, p.err);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t b = rows + n % ST * STAGE;
 #pragma unroll
-            for (int kk = 0; kk < BS / 16; ++kk)
-              umma_bf16_ts(tmem + ACC, t + kk * 8, rows_desc(q + C::BLOCK, BS, kk), id_a, (kk > 0) | (m > 0));
-#pragma unroll
-            for (int kk = 0; kk < BS / 16; ++kk)
-              umma_bf16_ts(tmem + ACC + C::COLS, t + BS + kk * 8, rows_desc(q, BS, kk), id_a,
-                           (kk > 0) | (m > 0));
-            umma_commit(&q_empty[st]);
-            if (n == steps) umma_commit(acc_full);
-          }
-        }
+        for (int kk = 0; kk < BT / 16; ++kk)
+          mma_ts(tmem + acc, tmem + t + (kk >> 1) * C::MC + (kk & 1) * 8, b + rows_step(kk), id_a,
+                 (kk > 0) | (n > 0), issue);
+        mma_commit(&empty[n % ST], issue);
+      };
+      scores(0, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+      scores(0, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
+      for (int n = 0; ok && n < steps; ++n) {
+        add(n, m.p_full, 0, T_DV, rows_b, m.b_empty);
+        if (n + 1 < steps) scores(n + 1, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+        add(n, m.ds_full, T_DP, T_DK, rows_a, m.a_empty);
+        if (n + 1 < steps) scores(n + 1, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
       }
-      if (lane == 0) umma_commit(mma_done);
-      warp_wait(mma_done, 0, abort_flag, p.err);  // before tensor memory is freed
+      if (ok) mma_commit(m.acc_full, issue);
+      mma_commit(m.mma_done, issue);
+      warp_wait(m.mma_done, 0, m.abort_flag, p.err);  // before tensor memory is freed
     }
   } else {
     set_regs_inc<C::REGS_MATH>();
-    // ------------------------------------------------ P^T and dS^T, a key per thread
+    // ------------------------------------------------ P^T, dS^T: a thread holds 32 queries of a key row
     const int w = (warp - 4) >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t = tmem + lanes + w * 2 * BS;
+    const uint32_t t = tmem + lanes + w * 32;
     const float c2 = p.scale * kAttnLog2e;
     int lo, hi;  // queries that see this thread's key
     queries_of(p, sq, key0 + r, lo, hi);
-    // Queries that see every key of the tile: blocks inside need no mask.
-    const int full0 = ra, full1 = rb;
-    // lse and delta of a block, a copy per warp: warps wait for nothing but their barriers
-    float* buf = rows + (warp - 4) * 2 * BS;
+    const uint32_t count = static_cast<uint32_t>(hi - lo);
+    // lse and delta of the warp's 32 queries, a copy per warp: warps wait for nothing but
+    // their barriers; the next block's values are on their way while this one is worked on
+    float* buf = m.rows + (warp - 4) * 2 * C::MC;
+    float nl, nd;
+    auto fetch = [&](int n) {
+      const int head = kv_head * p.group + n / nb, i = (j0 + n % nb) * BT + w * 32 + lane;
+      nl = nd = 0.0f;
+      if (i < sq.nq) {
+        const int64_t at = head * p.Tq + sq.q0 + i;
+        const float l = p.lse[at];
+        nl = l == -INFINITY ? 0.0f : -l * kAttnLog2e;  // (no key: every place is masked below)
+        nd = -p.delta[at];
+      }
+    };
+    if (steps > 0) fetch(0);
+    const float2 cc = make_float2(c2, c2);
     bool ok = true;
-    for (int n = w; n < steps; n += 2) {
-      const int head = kv_head * p.group + n / nb, i0 = (j0 + n % nb) * BS;
+    for (int n = 0; n < steps; ++n) {
+      const int i0 = (j0 + n % nb) * BT;
       __syncwarp();  // the previous block's values are read
-#pragma unroll
-      for (int e = 0; e < BS / 32; ++e) {
-        const int k = e * 32 + lane;
-        const bool live = i0 + k < sq.nq;
-        const int64_t at = head * p.Tq + sq.q0 + i0 + k;
-        buf[k] = live ? -p.lse[at] * kAttnLog2e : 0.0f;
-        buf[BS + k] = live ? -p.delta[at] : 0.0f;
-      }
+      buf[lane] = nl;
+      buf[C::MC + lane] = nd;
       __syncwarp();
-      if (!warp_wait(&s_full[w], (n >> 1) & 1, abort_flag, p.err)) { ok = false; break; }
+      if (n + 1 < steps) fetch(n + 1);
+      if (!warp_wait(m.s_full, n & 1, m.abort_flag, p.err)) { ok = false; break; }
       tc_fence_after();
-      const bool masked = i0 < full0 || i0 + BS > full1;
-      const float2 cc = make_float2(c2, c2);
+      uint32_t s[32], pk[16];
+      tmem_ld32(t, s);
+      tmem_ld_wait();
+      if (i0 < full0 || i0 + BT > full1) {
+        const int a = lo - i0 - w * 32;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t s[32], g[32], pp[16], pd[16];
-        tmem_ld32(t + c * 32, s);
-        tmem_ld32(t + BS + c * 32, g);
-        tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          const float4 nl = *reinterpret_cast<const float4*>(buf + c * 32 + k);
-          const float4 nd = *reinterpret_cast<const float4*>(buf + BS + c * 32 + k);
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float2 x = fma2(make_float2(__uint_as_float(s[k + e]), __uint_as_float(s[k + e + 1])), cc,
-                                  e ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y));
-            const float2 y = add2(make_float2(__uint_as_float(g[k + e]), __uint_as_float(g[k + e + 1])),
-                                  e ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y));
-            float2 pr = make_float2(attn_exp2(x.x), attn_exp2(x.y));
-            float2 ds = mul2(pr, y);
-            if (masked) {
-              const uint32_t cnt = static_cast<uint32_t>(hi - lo);
-              const int a = i0 + c * 32 + k + e - lo;
-              if (static_cast<uint32_t>(a) >= cnt) pr.x = ds.x = 0.0f;
-              if (static_cast<uint32_t>(a + 1) >= cnt) pr.y = ds.y = 0.0f;
-            }
-            pp[(k + e) / 2] = pack2(pr.x, pr.y);
-            pd[(k + e) / 2] = pack2(ds.x, ds.y);
-          }
-        }
-        // columns 16 c .. 16 c + 15: read already (the halves go in order)
-        tmem_st16(t + c * 16, pp);
-        tmem_st16(t + BS + c * 16, pd);
+        for (int k = 0; k < 32; ++k)
+          if (static_cast<uint32_t>(k - a) >= count) s[k] = 0xff800000u;  // -inf
       }
+      float2 pr[16];
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        const float4 l = *reinterpret_cast<const float4*>(buf + 2 * k);
+        const float2 x = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), cc,
+                              make_float2(l.x, l.y));
+        const float2 y = fma2(make_float2(__uint_as_float(s[2 * k + 2]), __uint_as_float(s[2 * k + 3])), cc,
+                              make_float2(l.z, l.w));
+        pr[k] = make_float2(attn_exp2(x.x), attn_exp2(x.y));
+        pr[k + 1] = make_float2(attn_exp2(y.x), attn_exp2(y.y));
+        pk[k] = pack2(pr[k].x, pr[k].y);
+        pk[k + 1] = pack2(pr[k + 1].x, pr[k + 1].y);
+      }
+      tmem_st16(t, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ds_full[w]);
+      if (lane == 0) mbar_arrive(m.p_full);
+      if (!warp_wait(m.dp_full, n & 1, m.abort_flag, p.err)) { ok = false; break; }
+      tc_fence_after();
+      tmem_ld32(t + T_DP, s);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        const float4 d = *reinterpret_cast<const float4*>(buf + C::MC + 2 * k);
+        const float2 x = mul2(pr[k], add2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])),
+                                          make_float2(d.x, d.y)));
+        const float2 y = mul2(pr[k + 1], add2(make_float2(__uint_as_float(s[2 * k + 2]), __uint_as_float(s[2 * k + 3])),
+                                              make_float2(d.z, d.w)));
+        pk[k] = pack2(x.x, x.y);
+        pk[k + 1] = pack2(y.x, y.y);
+      }
+      tmem_st16(t + T_DP, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(m.ds_full);
     }
-    if (ok && steps > 0) ok = warp_wait(acc_full, 0, abort_flag, p.err);
+    if (ok && steps > 0) ok = warp_wait(m.acc_full, 0, m.abort_flag, p.err);
     tc_fence_after();
-    if (ok) {  // the first warpgroup writes dV, the second dK
+    if (ok) {  // the even warpgroups write dV, the odd ones dK, half a row each
       const int64_t at = sq.k0 + key0 + r;
       const bool write = key0 + r < sq.nk;
-      if (w == 0)
-        store_row(static_cast<__nv_bfloat16*>(p.dV) + at * p.lddv + kv_head * p.hd, tmem + lanes + ACC, p.hd,
-                  1.0f, steps > 0, write);
+      if ((w & 1) == 0)
+        store_row(static_cast<__nv_bfloat16*>(p.dV) + at * p.lddv + kv_head * p.hd, tmem + lanes + T_DV, p.hd,
+                  1.0f, steps > 0, write, w >> 1, 2);
       else
-        store_row(static_cast<__nv_bfloat16*>(p.dK) + at * p.lddk + kv_head * p.hd,
-                  tmem + lanes + ACC + C::COLS, p.hd, p.scale, steps > 0, write);
+        store_row(static_cast<__nv_bfloat16*>(p.dK) + at * p.lddk + kv_head * p.hd, tmem + lanes + T_DK, p.hd,
+                  p.scale, steps > 0, write, w >> 1, 2);
     }
     tc_fence_before();
   }
@@ -545,31 +566,31 @@ int launch(const AttnArgs& a, cudaStream_t s) {
   using C = Cfg<NC>;
   const int kv_heads = a.heads / a.group;
   static std::atomic<uint64_t> dq_done{0}, dkv_done{0};
-  int rc = allow_smem(reinterpret_cast<const void*>(attn_dq_kernel<NC>), C::DQ_SMEM, dq_done);
-  if (!rc) rc = allow_smem(reinterpret_cast<const void*>(attn_dkv_kernel<NC>), C::KV_SMEM, dkv_done);
+  int rc = allow_smem(reinterpret_cast<const void*>(attn_dq_kernel<NC>), C::SMEM, dq_done);
+  if (!rc) rc = allow_smem(reinterpret_cast<const void*>(attn_dkv_kernel<NC>), C::SMEM, dkv_done);
   if (rc) return rc;
   CUtensorMap mq, mo, mk, mv;
   const int64_t lists = static_cast<int64_t>(a.heads) * a.batch;
-  const int64_t qb = (static_cast<int64_t>(a.max_q) + 2 * BT - 1) / (2 * BT);
+  const int64_t qb = (static_cast<int64_t>(a.max_q) + BT - 1) / BT;
   const int64_t kb = (static_cast<int64_t>(a.max_k) + BT - 1) / BT;
   if (qb > 65535 || kb > 65535 || lists > (1ll << 31) - 1) return QAT_ERR_SHAPE;
   if (a.Tq > 0 && qb > 0) {
     if ((rc = make_head_map(&mq, a.Q, a.hd, a.heads, a.Tq, a.ldq, BT))) return rc;
     if ((rc = make_head_map(&mo, a.dO, a.hd, a.heads, a.Tq, a.lddo, BT))) return rc;
-    if ((rc = make_head_map(&mk, a.K, a.hd, kv_heads, std::max<int64_t>(a.Tk, 1), a.ldk, BS))) return rc;
-    if ((rc = make_head_map(&mv, a.V, a.hd, kv_heads, std::max<int64_t>(a.Tk, 1), a.ldv, BS))) return rc;
+    if ((rc = make_head_map(&mk, a.K, a.hd, kv_heads, std::max<int64_t>(a.Tk, 1), a.ldk, BT))) return rc;
+    if ((rc = make_head_map(&mv, a.V, a.hd, kv_heads, std::max<int64_t>(a.Tk, 1), a.ldv, BT))) return rc;
     attn_dq_kernel<NC><<<dim3(static_cast<unsigned>(lists), static_cast<unsigned>(qb)), C::THREADS,
-                         C::DQ_SMEM, s>>>(mq, mo, mk, mv, a);
+                         C::SMEM, s>>>(mq, mo, mk, mv, a);
     count_launch();
     if (cudaGetLastError() != cudaSuccess) return QAT_ERR_CUDA;
   }
   if (a.Tk > 0 && kb > 0) {
-    if ((rc = make_head_map(&mq, a.Q, a.hd, a.heads, std::max<int64_t>(a.Tq, 1), a.ldq, BS))) return rc;
-    if ((rc = make_head_map(&mo, a.dO, a.hd, a.heads, std::max<int64_t>(a.Tq, 1), a.lddo, BS))) return rc;
+    if ((rc = make_head_map(&mq, a.Q, a.hd, a.heads, std::max<int64_t>(a.Tq, 1), a.ldq, BT))) return rc;
+    if ((rc = make_head_map(&mo, a.dO, a.hd, a.heads, std::max<int64_t>(a.Tq, 1), a.lddo, BT))) return rc;
     if ((rc = make_head_map(&mk, a.K, a.hd, kv_heads, a.Tk, a.ldk, BT))) return rc;
     if ((rc = make_head_map(&mv, a.V, a.hd, kv_heads, a.Tk, a.ldv, BT))) return rc;
     attn_dkv_kernel<NC><<<dim3(static_cast<unsigned>(lists / a.group), static_cast<unsigned>(kb)), C::THREADS,
-                          C::KV_SMEM, s>>>(mq, mo, mk, mv, a);
+                          C::SMEM, s>>>(mq, mo, mk, mv, a);
     count_launch();
     if (cudaGetLastError() != cudaSuccess) return QAT_ERR_CUDA;
   }

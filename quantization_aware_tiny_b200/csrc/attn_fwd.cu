@@ -66,14 +66,18 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   static_assert((1 + 4 * C::ST + 7) * 8 + 8 <= 256, "barrier block overflow");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int head = static_cast<int>(blockIdx.x % p.heads);
   const Seq sq = seq_of(p, static_cast<int>(blockIdx.x / p.heads));
   // late query blocks see most keys under a causal mask: they start first
   const int i0 = static_cast<int>(gridDim.y - 1 - blockIdx.y) * 2 * BQ;
   if (i0 >= sq.nq) return;
   int b0[2], b1[2], j0, j1;
-  key_blocks<BQ, BKV>(p, sq, i0, b0, b1, j0, j1);
+  key_blocks<BQ, BKV>(p, sq, i0, b0[0], b1[0]);
+  key_blocks<BQ, BKV>(p, sq, i0 + BQ, b0[1], b1[1]);
+  j0 = b1[0] > b0[0] ? b0[0] : b0[1];
+  if (b1[1] > b0[1]) j0 = min(j0, b0[1]);
+  j1 = max(max(b1[0], b1[1]), j0);
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -145,12 +149,14 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    // -------------------------------------------------- MMA issuer (the warp
-    // walks together; lane 0 issues)
+    // -------------------------------------------------- MMA issuer
     if (j1 > j0) {
       const int ks = (p.hd + 15) / 16;
       const uint32_t id_s = idesc_bf16(BQ, BKV, false, false);
       const uint32_t id_o = idesc_bf16(BQ, ks * 16, false, true);
+      const uint32_t issue = elect_lane();
+      const uint64_t dq = kmajor_desc<BQ>(sQ), dk = kmajor_desc<BKV>(sK), dv = rows_desc<BKV>(sV);
+      constexpr uint32_t STAGE = C::TILE >> 4;
       bool ok = warp_wait(q_full, 0, abort_flag, p.err);
       uint32_t pph[2] = {0, 0};
       for (int j = j0; ok && j <= j1; ++j) {
@@ -163,36 +169,27 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
             pph[w] ^= 1u;
             if (!ok) break;
             tc_fence_after();
-            uint8_t* v = sV + pst * C::TILE;
             const int rows = sq.nk - (j - 1) * BKV;
-            if (rows < BKV) clear_rows<NC>(v, BKV, rows, lane);
-            if (lane == 0) {
-              const uint32_t acc0 = j - 1 > b0[w];
+            if (rows < BKV) clear_rows<NC>(sV + pst * C::TILE, BKV, rows, lane);
+            const uint32_t more = j - 1 > b0[w];
 #pragma unroll
-              for (int kk = 0; kk < BKV / 16; ++kk)
-                umma_bf16_ts(tmem + 256 + w * C::O_COLS, tmem + w * 128 + kk * 8,
-                             rows_desc(v, BKV, kk), id_o, (kk > 0) | acc0);
-              if (j == b1[w]) umma_commit(&o_full[w]);
-            }
+            for (int kk = 0; kk < BKV / 16; ++kk)
+              mma_ts(tmem + 256 + w * C::O_COLS, tmem + w * 128 + kk * 8, dv + pst * STAGE + rows_step(kk),
+                     id_o, (kk > 0) | more, issue);
+            if (j == b1[w]) mma_commit(&o_full[w], issue);
           }
           if (ok && j < j1 && j >= b0[w] && j < b1[w]) {  // S = Q K^T of block j
             ok = warp_wait(&k_full[st], (n / C::ST) & 1, abort_flag, p.err);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
-              for (int kk = 0; kk < ks; ++kk)
-                umma_bf16(tmem + w * 128, kmajor_desc(sQ + w * C::TILE, BQ, kk),
-                          kmajor_desc(sK + st * C::TILE, BKV, kk), id_s, kk > 0);
-              umma_commit(&s_full[w]);
-            }
+            product<NC, BQ>(tmem + w * 128, dq + w * STAGE, dk + st * STAGE, id_s, ks, issue);
+            mma_commit(&s_full[w], issue);
           }
         }
-        if (ok && lane == 0) {
-          if (j < j1) umma_commit(&k_empty[st]);
-          if (j > j0) umma_commit(&v_empty[pst]);
-        }
+        if (ok && j < j1) mma_commit(&k_empty[st], issue);
+        if (ok && j > j0) mma_commit(&v_empty[pst], issue);
       }
-      if (lane == 0) umma_commit(mma_done);
+      mma_commit(mma_done, issue);
       mbar_wait(mma_done, 0, abort_flag, p.err);  // before tensor memory is freed
     }
   }

@@ -31,14 +31,50 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T: A's rows are TMEM lanes, two bf16 per column.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// The MMA forms below are executed by a whole warp, with `issue` set in one lane
+// (the same one throughout): the code around them stays convergent, so the
+// descriptors live in uniform registers.  Issued from a branch of one lane, with
+// the descriptors built on the spot, an MMA took 90 to 180 cycles to issue,
+// longer than the 64 it runs for, and the issue bound every attention kernel
+// (dq, head size 64: 2,250 of 2,900 cycles a block).
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r;
+}
+// D[tmem] (+)= A[smem] * B[smem]^T
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issue));
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T: A's rows are TMEM lanes, two bf16 per column.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issue));
+}
+// Arrive once on `bar` when every MMA issued so far by the issuing lane completes.
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(issue)
+      : "memory");
 }
 
 // Each lane of the warp writes 32 / 16 consecutive columns of its own TMEM lane.
@@ -152,27 +188,17 @@ __device__ __forceinline__ void queries_of(const AttnArgs& p, const Seq& s, int 
   lo = min(lo, hi);
 }
 
-// Key blocks [b0[w], b1[w]) that tiles w = 0, 1 of ROWS queries from i0 on see,
-// and [j0, j1), which covers both; a tile that sees nothing has b1 = b0.
+// Key blocks [b0, b1) that ROWS queries from i0 on see; none: b1 = b0.
 template <int ROWS, int KEYS>
-__device__ __forceinline__ void key_blocks(const AttnArgs& p, const Seq& s, int i0, int (&b0)[2],
-                                           int (&b1)[2], int& j0, int& j1) {
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int first = i0 + w * ROWS, last = min(first + ROWS, s.nq) - 1;
-    b0[w] = b1[w] = 0;
-    if (first < s.nq) {
-      int lo, hi, lo2, hi2;
-      keys_of(p, s, first, lo, hi);
-      keys_of(p, s, last, lo2, hi2);
-      // the last row sees furthest; where the first sees nothing, a later one starts at key 0
-      b0[w] = hi > lo ? lo / KEYS : 0;
-      b1[w] = hi2 > lo2 ? (hi2 + KEYS - 1) / KEYS : b0[w];
-    }
-  }
-  j0 = b1[0] > b0[0] ? b0[0] : b0[1];
-  if (b1[1] > b0[1]) j0 = min(j0, b0[1]);
-  j1 = max(max(b1[0], b1[1]), j0);
+__device__ __forceinline__ void key_blocks(const AttnArgs& p, const Seq& s, int i0, int& b0, int& b1) {
+  b0 = b1 = 0;
+  if (i0 >= s.nq) return;
+  int lo, hi, lo2, hi2;
+  keys_of(p, s, i0, lo, hi);
+  keys_of(p, s, min(i0 + ROWS, s.nq) - 1, lo2, hi2);
+  // the last row sees furthest; where the first sees nothing, a later one starts at key 0
+  b0 = hi > lo ? lo / KEYS : 0;
+  b1 = hi2 > lo2 ? (hi2 + KEYS - 1) / KEYS : b0;
 }
 
 // Bytes of a tile of `rows` rows and NC 64-dim chunks; chunk c starts at c * rows * 128.
@@ -194,13 +220,31 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int rows, int from, in
   __syncwarp();
 }
 
-// K-major operand descriptor of k-step kk (16 dims) of a staged tile of `rows` rows.
-__device__ __forceinline__ uint64_t kmajor_desc(const uint8_t* tile, int rows, int kk) {
-  return sw128_desc(smem_u32(tile) + (kk >> 2) * rows * 128 + (kk & 3) * 32, 16, 1024);
+// Descriptors of staged tiles of ROWS rows.  K-major: the contraction runs over a
+// row's dims, k-step kk (16 dims) adds kmajor_step(kk).  By rows: it runs over the
+// tile's rows, k-step kk (rows 16 kk .. 16 kk + 15) adds rows_step(kk).  (The address
+// sits in the descriptor's low bits in units of 16 bytes.)
+template <int ROWS>
+__device__ __forceinline__ uint64_t kmajor_desc(const uint8_t* tile) {
+  return sw128_desc(smem_u32(tile), 16, 1024);
 }
-// MN-major descriptor (the contraction runs over the tile's rows) of rows 16 kk .. 16 kk + 15.
-__device__ __forceinline__ uint64_t rows_desc(const uint8_t* tile, int rows, int kk) {
-  return sw128_desc(smem_u32(tile) + kk * 2048, rows * 128, 1024);
+template <int ROWS>
+__device__ __forceinline__ constexpr uint32_t kmajor_step(int kk) {
+  return ((kk >> 2) * ROWS * 128 + (kk & 3) * 32) >> 4;
+}
+template <int ROWS>
+__device__ __forceinline__ uint64_t rows_desc(const uint8_t* tile) {
+  return sw128_desc(smem_u32(tile), ROWS * 128, 1024);
+}
+__device__ __forceinline__ constexpr uint32_t rows_step(int kk) { return (kk * 2048) >> 4; }
+
+// D = A B^T over the 16-dim steps of the head (at most 4 NC), both operands K-major tiles.
+template <int NC, int ROWS>
+__device__ __forceinline__ void product(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                        int ks, uint32_t issue) {
+#pragma unroll
+  for (int kk = 0; kk < 4 * NC; ++kk)
+    if (kk < ks) mma_ss(d_tmem, a + kmajor_step<ROWS>(kk), b + kmajor_step<ROWS>(kk), idesc, kk > 0, issue);
 }
 
 }  // namespace qat

@@ -143,19 +143,23 @@ def _check(rc, where):
         raise QatError(rc, where)
 
 
+# Addresses go to ctypes as plain integers (the argument types are declared once,
+# in lib()) and the current stream as the handle torch keeps: a call of a few
+# microseconds on the device is otherwise paid twice over here.
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ws(ws):
     if ws is None:
         return None, 0
-    return ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 class QWeight:
