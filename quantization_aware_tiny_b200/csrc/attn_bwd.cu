@@ -52,7 +52,7 @@ struct Smem {
   uint8_t *fix_a, *fix_b, *ring_a, *ring_b;
   float* rows;
   uint64_t *fix_full, *a_full, *a_empty, *b_full, *b_empty;
-  uint64_t *s_full, *dp_full, *p_full, *ds_full, *acc_full, *mma_done;
+  uint64_t *s_full, *dp_full, *s_read, *p_full, *p_free, *ds_full, *acc_full, *mma_done;
   uint32_t* tmem_slot;
   volatile int* abort_flag;
 
@@ -69,13 +69,15 @@ struct Smem {
     b_empty = b_full + C::ST;
     s_full = b_empty + C::ST;
     dp_full = s_full + 1;
-    p_full = dp_full + 1;
-    ds_full = p_full + 1;
+    s_read = dp_full + 1;
+    p_full = s_read + 1;
+    p_free = p_full + 1;
+    ds_full = p_free + 1;
     acc_full = ds_full + 1;
     mma_done = acc_full + 1;
     tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((1 + 4 * C::ST + 6) * 8 + 8 <= 256, "barrier block overflow");
+    static_assert((1 + 4 * C::ST + 8) * 8 + 8 <= 256, "barrier block overflow");
   }
   __device__ void init() {
     mbar_init(fix_full, 1);
@@ -87,7 +89,9 @@ struct Smem {
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
-    mbar_init(p_full, 4 * C::GROUPS);  // the math warps
+    mbar_init(s_read, 4 * C::GROUPS);  // the math warps
+    mbar_init(p_full, 4 * C::GROUPS);
+    mbar_init(p_free, 1);
     mbar_init(ds_full, 4 * C::GROUPS);
     mbar_init(acc_full, 1);
     mbar_init(mma_done, 1);
@@ -103,26 +107,17 @@ __device__ __forceinline__ void load_tile(const CUtensorMap* map, uint64_t* bar,
   for (int c = 0; c < NC; ++c) tma_load_3d(map, bar, dst + c * BT * 128, c * 64, head, row);
 }
 
-// bf16(a * f) of one accumulator row of hd columns, from tensor memory to global:
-// its 32-column pieces from, from + step, ...
-__device__ __forceinline__ void store_row(__nv_bfloat16* out, uint32_t t, int hd, float f, bool any,
-                                          bool write, int from, int step) {
+// The warp's 32 rows of an accumulator (at t) times f, as bf16, to `out` (its first
+// row and the head's first column): the 32-column pieces from, from + step, ...
+__device__ __forceinline__ void store_rows(__nv_bfloat16* out, int64_t ld, uint32_t t, int hd, float f,
+                                           bool any, int live, int from, int step, uint8_t* stage, int lane) {
   for (int c = from; c < (hd + 31) / 32; c += step) {
-    uint32_t o[32];
+    uint32_t o[32] = {};
     if (any) {
       tmem_ld32(t + c * 32, o);
       tmem_ld_wait();
     }
-    if (!write) continue;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = any ? __uint_as_float(o[g * 8 + k]) * f : 0.0f;
-      if (c * 32 + g * 8 < hd)
-        *reinterpret_cast<uint4*>(out + c * 32 + g * 8) =
-            make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-    }
+    store_piece(out + c * 32, ld, o, f, hd - c * 32, live, smem_u32(stage), lane);
   }
 }
 
@@ -229,7 +224,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       dprobs(0);
       for (int n = 0; ok && n < steps; ++n) {
         if (n + 1 < steps) {
-          ok = warp_wait(m.p_full, n & 1, m.abort_flag, p.err);  // S(n) has been read
+          ok = warp_wait(m.s_read, n & 1, m.abort_flag, p.err);
           scores(n + 1);
         }
         ok = ok && warp_wait(m.ds_full, n & 1, m.abort_flag, p.err);
@@ -260,32 +255,52 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     int full0, full1, unused;  // keys that every row of the tile sees
     keys_of(p, sq, i0, unused, full1);
     keys_of(p, sq, i0 + BT - 1, full0, unused);
-    float lse2 = 0.0f, delta = 0.0f;
+    float lse2 = 0.0f;
     if (i < sq.nq) {
       const float l = p.lse[head * p.Tq + at];
       lse2 = l == -INFINITY ? 0.0f : l * kAttnLog2e;  // (no key: every place is masked below)
-      const uint4* o = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.O) + at * p.ldo + head * p.hd);
-      const uint4* d = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dO) + at * p.lddo + head * p.hd);
-      float part[2] = {0.0f, 0.0f};
-#pragma unroll 4
-      for (int c = 0; c < p.hd / 8; ++c) {
-        const uint4 x = __ldg(o + c), y = __ldg(d + c);
-        const __nv_bfloat162* a = reinterpret_cast<const __nv_bfloat162*>(&x);
-        const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&y);
+    }
+    // delta = rowsum(dO * O): a warp takes 8 of the tile's rows, half a warp a row, all
+    // loads first; shared memory (and p_full, otherwise unused here) hands them round.
+    // (A thread per row, 16 bytes at a time, took 20,000 cycles.)
+    {
+      const int r0 = (warp - 4) * 8 + (lane >> 4), e = (lane & 15) * 8;
+      uint4 x[4], y[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 u = __bfloat1622float2(a[k]), v = __bfloat1622float2(b[k]);
-          part[0] = fmaf(u.x, v.x, part[0]);
-          part[1] = fmaf(u.y, v.y, part[1]);
+      for (int k = 0; k < 4; ++k) {
+        x[k] = y[k] = make_uint4(0, 0, 0, 0);
+        const int64_t row = sq.q0 + i0 + r0 + 2 * k;
+        if (i0 + r0 + 2 * k < sq.nq && e < p.hd) {
+          x[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.O) + row * p.ldo + head * p.hd + e));
+          y[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dO) + row * p.lddo + head * p.hd + e));
         }
       }
-      delta = part[0] + part[1];
-      if (w == 0) p.delta[head * p.Tq + at] = delta;  // for the other kernel
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat162* a = reinterpret_cast<const __nv_bfloat162*>(&x[k]);
+        const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&y[k]);
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2 u = __bfloat1622float2(a[c]), v = __bfloat1622float2(b[c]);
+          sum = fmaf(u.x, v.x, fmaf(u.y, v.y, sum));
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const int r = r0 + 2 * k;
+        if ((lane & 15) == 0) {
+          m.rows[r] = sum;
+          if (i0 + r < sq.nq) p.delta[head * p.Tq + sq.q0 + i0 + r] = sum;  // for the other kernel
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(m.p_full);
     }
+    bool ok = warp_wait(m.p_full, 0, m.abort_flag, p.err);
+    const float delta = m.rows[quarter * 32 + lane];
     const float2 cc = make_float2(c2, c2), nl = make_float2(-lse2, -lse2), nd = make_float2(-delta, -delta);
     const uint32_t count = static_cast<uint32_t>(hi - lo);
-    bool ok = true;
-    for (int n = 0; n < steps; ++n) {
+    for (int n = 0; ok && n < steps; ++n) {
       if (!warp_wait(m.s_full, n & 1, m.abort_flag, p.err)) { ok = false; break; }
       tc_fence_after();
       uint32_t s[32];
@@ -293,7 +308,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(m.p_full);
+      if (lane == 0) mbar_arrive(m.s_read);
       const int key0 = (j0 + n) * BT;
       if (key0 < full0 || key0 + BT > full1) {
         const int a = lo - key0 - w * 32;
@@ -326,9 +341,11 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     }
     if (ok && steps > 0) ok = warp_wait(m.acc_full, 0, m.abort_flag, p.err);
     tc_fence_after();
-    if (ok)  // the warpgroups store a quarter of the row each
-      store_row(static_cast<__nv_bfloat16*>(p.dQ) + at * p.lddq + head * p.hd, t + T_DQ, p.hd, p.scale,
-                steps > 0, i < sq.nq, w, C::GROUPS);
+    if (ok) {  // the warpgroups store a quarter of the row each
+      const int r0 = i0 + quarter * 32;
+      store_rows(static_cast<__nv_bfloat16*>(p.dQ) + (sq.q0 + r0) * p.lddq + head * p.hd, p.lddq, t + T_DQ, p.hd,
+                 p.scale, steps > 0, sq.nq - r0, w, C::GROUPS, m.fix_a + (warp - 4) * 2048, lane);
+    }
     tc_fence_before();
   }
   __syncthreads();
@@ -341,9 +358,11 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
 // -------------------------------------------------------------------- dK, dV
 
 // A CTA owns 128 keys of a key head.  Tensor memory: S^T and dP^T (128 columns
-// each; P^T and dS^T replace them as bf16, each warpgroup within the columns it
-// reads), dV, dK.  Issue order: dV += P^T(n) dO(n) and S^T(n + 1) once P(n) is
-// written, dK += dS^T(n) Q(n) and dP^T(n + 1) once dS(n) is.
+// each; dS^T replaces dP^T as bf16, each warpgroup within the columns it reads),
+// P^T, dV, dK.  Issue order: S^T(n + 1) once S^T(n) is read; dV += P^T(n) dO(n)
+// once P(n) is written; dK += dS^T(n) Q(n) and dP^T(n + 1) once dS(n) is.
+// Heads of more than 96 dims leave no columns for P^T: it then replaces S^T, and
+// S^T(n + 1) waits for dV's product (a separate P^T at head size 80: see below).
 template <int NC>
 __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     attn_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
@@ -351,8 +370,11 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
                     const AttnArgs p) {
   using C = Cfg<NC>;
   constexpr int ST = C::ST;
-  constexpr uint32_t T_DP = BT, T_DV = 2 * BT, T_DK = 2 * BT + C::COLS;
-  static_assert(T_DK + C::COLS <= 512, "tensor memory");
+  constexpr uint32_t T_DP = BT;
+  const int ks = (p.hd + 15) / 16;
+  const bool apart = ks <= 6;  // 2 * 128 + 64 + 2 * 96 = 512 columns
+  const uint32_t t_p = apart ? 2 * BT : 0, p_step = apart ? 16 : C::MC;  // a warpgroup's P^T columns
+  const uint32_t t_dv = apart ? 2 * BT + BT / 2 : 2 * BT, t_dk = t_dv + (apart ? ks * 16 : C::COLS);
   extern __shared__ uint8_t smem_raw[];
   const Smem<NC> m(smem_raw);  // fixed: K, V; rings: Q, dO
 
@@ -412,7 +434,6 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       for (int n = max(0, nb_ - ST); n < nb_; ++n) mbar_drain(&m.b_full[n % ST], (n / ST) & 1);
     } else if (warp == 1 && steps > 0) {
       // ------------------------------------------------ MMA issuer
-      const int ks = (p.hd + 15) / 16;
       const uint32_t id_s = idesc_bf16(BT, BT, false, false);
       const uint32_t id_a = idesc_bf16(BT, ks * 16, false, true);
       const uint32_t issue = elect_lane();
@@ -432,23 +453,30 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
         mma_commit(done, issue);
       };
       // accumulator += (bf16 probabilities at t) . streamed rows of step n
-      auto add = [&](int n, uint64_t* ready, uint32_t t, uint32_t acc, uint64_t rows, uint64_t* empty) {
+      auto add = [&](int n, uint64_t* ready, uint32_t t, uint32_t t_step, uint32_t acc, uint64_t rows,
+                     uint64_t* empty) {
         ok = ok && warp_wait(ready, n & 1, m.abort_flag, p.err);
         if (!ok) return;
         tc_fence_after();
         const uint64_t b = rows + n % ST * STAGE;
 #pragma unroll
         for (int kk = 0; kk < BT / 16; ++kk)
-          mma_ts(tmem + acc, tmem + t + (kk >> 1) * C::MC + (kk & 1) * 8, b + rows_step(kk), id_a,
+          mma_ts(tmem + acc, tmem + t + (kk >> 1) * t_step + (kk & 1) * 8, b + rows_step(kk), id_a,
                  (kk > 0) | (n > 0), issue);
         mma_commit(&empty[n % ST], issue);
       };
       scores(0, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
       scores(0, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
       for (int n = 0; ok && n < steps; ++n) {
-        add(n, m.p_full, 0, T_DV, rows_b, m.b_empty);
-        if (n + 1 < steps) scores(n + 1, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
-        add(n, m.ds_full, T_DP, T_DK, rows_a, m.a_empty);
+        const bool more = n + 1 < steps;
+        if (apart && more) {
+          ok = warp_wait(m.s_read, n & 1, m.abort_flag, p.err);
+          scores(n + 1, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+        }
+        add(n, m.p_full, t_p, p_step, t_dv, rows_b, m.b_empty);
+        if (ok) mma_commit(m.p_free, issue);
+        if (!apart && more) scores(n + 1, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+        add(n, m.ds_full, T_DP, C::MC, t_dk, rows_a, m.a_empty);
         if (n + 1 < steps) scores(n + 1, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
       }
       if (ok) mma_commit(m.acc_full, issue);
@@ -496,6 +524,11 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       uint32_t s[32], pk[16];
       tmem_ld32(t, s);
       tmem_ld_wait();
+      if (apart) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(m.s_read);
+      }
       if (i0 < full0 || i0 + BT > full1) {
         const int a = lo - i0 - w * 32;
 #pragma unroll
@@ -515,7 +548,10 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
         pk[k] = pack2(pr[k].x, pr[k].y);
         pk[k + 1] = pack2(pr[k + 1].x, pr[k + 1].y);
       }
-      tmem_st16(t, pk);
+      // (P of the block before has been multiplied long since)
+      if (n > 0 && !warp_wait(m.p_free, (n - 1) & 1, m.abort_flag, p.err)) { ok = false; break; }
+      tc_fence_after();
+      tmem_st16(tmem + lanes + t_p + w * p_step, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -543,14 +579,15 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     if (ok && steps > 0) ok = warp_wait(m.acc_full, 0, m.abort_flag, p.err);
     tc_fence_after();
     if (ok) {  // the even warpgroups write dV, the odd ones dK, half a row each
-      const int64_t at = sq.k0 + key0 + r;
-      const bool write = key0 + r < sq.nk;
+      const int r0 = key0 + quarter * 32;
+      const int64_t at = sq.k0 + r0;
+      uint8_t* stage = m.fix_a + (warp - 4) * 2048;
       if ((w & 1) == 0)
-        store_row(static_cast<__nv_bfloat16*>(p.dV) + at * p.lddv + kv_head * p.hd, tmem + lanes + T_DV, p.hd,
-                  1.0f, steps > 0, write, w >> 1, 2);
+        store_rows(static_cast<__nv_bfloat16*>(p.dV) + at * p.lddv + kv_head * p.hd, p.lddv, tmem + lanes + t_dv, p.hd,
+                   1.0f, steps > 0, sq.nk - r0, w >> 1, 2, stage, lane);
       else
-        store_row(static_cast<__nv_bfloat16*>(p.dK) + at * p.lddk + kv_head * p.hd, tmem + lanes + T_DK, p.hd,
-                  p.scale, steps > 0, write, w >> 1, 2);
+        store_rows(static_cast<__nv_bfloat16*>(p.dK) + at * p.lddk + kv_head * p.hd, p.lddk, tmem + lanes + t_dk, p.hd,
+                   p.scale, steps > 0, sq.nk - r0, w >> 1, 2, stage, lane);
     }
     tc_fence_before();
   }

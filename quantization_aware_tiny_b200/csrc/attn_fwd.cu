@@ -239,9 +239,9 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       float mx[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        mx[c] = __uint_as_float(s[c][0]);
+        mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
-        for (int k = 1; k < 32; ++k) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][k]));
+        for (int k = 2; k < 32; k += 2) mx[c] = max3(mx[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
       }
       const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       const bool grow = (mb - m) * c2 > C::RESCALE || m == -INFINITY;
@@ -262,20 +262,22 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       }
       m = mn;
       const float mc = m == -INFINITY ? 0.0f : m * c2;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const float2 cc = make_float2(c2, c2), nm = make_float2(-mc, -mc);
+      float2 sum[4] = {};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
-          const float x = attn_exp2(fmaf(__uint_as_float(s[c][k]), c2, -mc));
-          const float y = attn_exp2(fmaf(__uint_as_float(s[c][k + 1]), c2, -mc));
-          sum[c] += x + y;
-          pk[k / 2] = pack2(x, y);
+          float2 x = fma2(make_float2(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), cc, nm);
+          x = make_float2(attn_exp2(x.x), attn_exp2(x.y));
+          sum[c] = add2(sum[c], x);
+          pk[k / 2] = pack2(x.x, x.y);
         }
         tmem_st16(t_s + c * 16, pk);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+      l += both.x + both.y;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -283,32 +285,29 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     }
     const bool any = b1[w] > b0[w];
     if (ok && any) ok = warp_wait(&o_full[w], 0, abort_flag, p.err);
+    // (the row's way out is Q's place: a tile that sees nothing still has its Q on the way)
+    if (ok && j1 > j0) ok = warp_wait(q_full, 0, abort_flag, p.err);
     tc_fence_after();
     if (ok && i0 + w * BQ < sq.nq) {  // the same for all rows of the tile
       const bool none = l == 0.0f;  // the mask leaves the row no key
       const float inv = none ? 0.0f : 1.0f / l;
-      const int64_t at = sq.q0 + i;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.O) + at * p.ldo + head * p.hd;
+      const int r0 = i0 + w * BQ + quarter * 32;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.O) + (sq.q0 + r0) * p.ldo + head * p.hd;
+      const uint32_t stage = smem_u32(sQ) + w * C::TILE + quarter * 2048;  // (Q has been multiplied)
       for (int c = 0; c < ocols; ++c) {
-        uint32_t o[32];
+        uint32_t o[32] = {};
         if (any) {
           tmem_ld32(t_o + c * 32, o);
           tmem_ld_wait();
-        }
-        if (i < sq.nq) {
+          if (none) {  // (0 * NaN of a place that the mask leaves out)
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = none ? 0.0f : __uint_as_float(o[g * 8 + k]) * inv;
-            if (c * 32 + g * 8 < p.hd)
-              *reinterpret_cast<uint4*>(out + c * 32 + g * 8) =
-                  make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+            for (int k = 0; k < 32; ++k) o[k] = 0;
           }
         }
+        store_piece(out + c * 32, p.ldo, o, inv, p.hd - c * 32, sq.nq - r0, stage, lane);
       }
       if (i < sq.nq)
-        p.lse[head * p.Tq + at] = none ? -INFINITY : fmaf(m, p.scale, logf(l));
+        p.lse[head * p.Tq + sq.q0 + i] = none ? -INFINITY : fmaf(m, p.scale, logf(l));
     }
     tc_fence_before();
   }
