@@ -136,6 +136,67 @@ __device__ __forceinline__ void set_regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// ---- work stealing.  A kernel is launched with one block per piece of work; a
+// running block takes over pieces whose blocks have not started, so its set-up is
+// paid once and the next piece's loads run below this one's last products.  The
+// hardware hands pieces out in launch order, longest first here.
+struct Work {
+  int list, block;  // blockIdx.x, blockIdx.y of the piece
+};
+// Asks for a piece; the answer (16 bytes) completes on `bar`.  One thread.
+__device__ __forceinline__ void work_ask(uint32_t answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          answer),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// Whether the answer is a piece, and which.
+__device__ __forceinline__ bool work_read(uint32_t answer, Work& w) {
+  uint32_t x = 0, y = 0, ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%3];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %2, 1, 0, p;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, %1, _, _}, r;\n\t}\n"
+      : "+r"(x), "+r"(y), "=r"(ok)
+      : "r"(answer)
+      : "memory");
+  w.list = static_cast<int>(x);
+  w.block = static_cast<int>(y);
+  return ok != 0;
+}
+// The answers' two slots: 32 bytes, and a full and an empty barrier each.
+struct WorkQueue {
+  uint32_t answers;
+  uint64_t *full, *empty;  // [2]
+
+  // Slot of the n-th answer is read by `readers` warps.
+  __device__ void init(int readers) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], readers);
+    }
+  }
+  // Asks for the (n + 1)-th piece (one thread, at the start of the n-th).
+  __device__ bool ask(int n, volatile int* abort_flag, int* err) {
+    if (n >= 2 && !mbar_wait(&empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, err)) return false;
+    work_ask(answers + (n & 1) * 16, &full[n & 1]);
+    return true;
+  }
+  // The piece after the n-th; false: there is none (or a wait ran out).  A whole warp.
+  __device__ bool next(int n, Work& w, int lane, volatile int* abort_flag, int* err) {
+    if (!warp_wait(&full[n & 1], (n >> 1) & 1, abort_flag, err)) return false;
+    const bool ok = work_read(answers + (n & 1) * 16, w);
+    fence_proxy_async_smem();  // read before the slot is written again
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[n & 1]);
+    return ok;
+  }
+};
+
 // ---- sequences
 struct Seq {
   int64_t q0, k0;  // first query / key row

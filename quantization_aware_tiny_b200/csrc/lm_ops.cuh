@@ -45,6 +45,7 @@ struct AttnArgs {
   const int32_t* cu_k;
   int batch, max_q, max_k;
   int heads, group, hd, causal, window;
+  int rows;  // forward of short queries: rows of a tile per head (0: tiles of one head)
   float scale;
   const void *Q, *K, *V, *dO;
   void* O;

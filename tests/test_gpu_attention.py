@@ -127,6 +127,26 @@ def test_fwd_queries_and_keys_of_other_lengths(lens, mask):
     Case(*lens, heads=2, kv_heads=2, hd=80, **mask).check_forward()
 
 
+@pytest.mark.parametrize("heads", [(8, 1, 64), (8, 2, 80), (6, 2, 128), (3, 1, 32), (5, 5, 64), (12, 1, 16)])
+@pytest.mark.parametrize("n", [1, 31, 33, 64, 65, 128])
+def test_fwd_few_queries_over_many_keys(heads, n):
+    """Heads of a group share a tile's rows, the two tiles share the keys: single
+    tokens, rows off the tile, key counts of one block, an odd and an even number."""
+    h, kv, hd = heads
+    for window in (0, 150):
+        Case([n, max(1, n // 2), n], [700, 100, 257], heads=h, kv_heads=kv, hd=hd, window=window).check_forward()
+
+
+def test_fwd_more_pieces_than_the_gpu_holds():
+    """Blocks take over pieces that have not started: thousands of them, empty ones among them."""
+    g = torch.Generator().manual_seed(0)
+    lens = torch.randint(0, 400, (300,), generator=g).tolist()
+    Case(lens, heads=4, kv_heads=2, hd=16).check_forward()
+    lq = torch.randint(0, 65, (700,), generator=g).tolist()
+    lk = torch.randint(0, 300, (700,), generator=g).tolist()
+    Case(lq, lk, heads=4, kv_heads=2, hd=16).check_forward()
+
+
 def test_fwd_equal_lengths_without_tables():
     Case([160] * 3, packed=False).check_forward()
     Case([64] * 3, [200] * 3, packed=False, hd=128).check_forward()
