@@ -41,7 +41,8 @@ struct Cfg {
   static constexpr int TILE = tile_bytes(BT, NC);
   static constexpr int ST = NC == 1 ? 4 : 2;        // stages of either ring
   static constexpr int ROWS_BYTES = 4 * GROUPS * 2 * MC * 4;  // dkv: lse and delta, per warp
-  static constexpr int SMEM = (2 + 2 * ST) * TILE + ROWS_BYTES + 1024 + 256;
+  static constexpr int OUT_BYTES = 4 * GROUPS * 1024;  // the gradient rows' way out, per warp
+  static constexpr int SMEM = (2 + 2 * ST) * TILE + ROWS_BYTES + OUT_BYTES + 1024 + 512;
   static constexpr int COLS = 64 * NC;              // tensor-memory columns of an accumulator
 };
 
@@ -49,9 +50,9 @@ struct Cfg {
 template <int NC>
 struct Smem {
   using C = Cfg<NC>;
-  uint8_t *fix_a, *fix_b, *ring_a, *ring_b;
+  uint8_t *fix_a, *fix_b, *ring_a, *ring_b, *out;
   float* rows;
-  uint64_t *fix_full, *a_full, *a_empty, *b_full, *b_empty;
+  uint64_t *fix_full, *fix_empty, *a_full, *a_empty, *b_full, *b_empty;
   uint64_t *s_full, *dp_full, *s_read, *p_full, *p_free, *ds_full, *acc_full, *mma_done;
   uint32_t* tmem_slot;
   volatile int* abort_flag;
@@ -62,8 +63,10 @@ struct Smem {
     ring_a = fix_b + C::TILE;
     ring_b = ring_a + C::ST * C::TILE;
     rows = reinterpret_cast<float*>(ring_b + C::ST * C::TILE);
-    fix_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(rows) + C::ROWS_BYTES);
-    a_full = fix_full + 1;
+    out = reinterpret_cast<uint8_t*>(rows) + C::ROWS_BYTES;
+    fix_full = reinterpret_cast<uint64_t*>(out + C::OUT_BYTES);
+    fix_empty = fix_full + 1;
+    a_full = fix_empty + 1;
     a_empty = a_full + C::ST;
     b_full = a_empty + C::ST;
     b_empty = b_full + C::ST;
@@ -75,11 +78,16 @@ struct Smem {
     ds_full = p_free + 1;
     acc_full = ds_full + 1;
     mma_done = acc_full + 1;
-    tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 5);
     abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((1 + 4 * C::ST + 8) * 8 + 8 <= 256, "barrier block overflow");
+    static_assert((2 + 4 * C::ST + 12) * 8 + 8 <= 512 - 32, "barrier block overflow");
+  }
+  __device__ WorkQueue queue() const {
+    return WorkQueue{smem_u32(fix_full) + 512 - 32, mma_done + 1, mma_done + 3};
   }
   __device__ void init() {
+    queue().init(2 + 4 * C::GROUPS);  // producer, MMA, math warps
+    mbar_init(fix_empty, 1);
     mbar_init(fix_full, 1);
     for (int i = 0; i < C::ST; ++i) {
       mbar_init(&a_full[i], 1);
@@ -108,16 +116,66 @@ __device__ __forceinline__ void load_tile(const CUtensorMap* map, uint64_t* bar,
 }
 
 // The warp's 32 rows of an accumulator (at t) times f, as bf16, to `out` (its first
-// row and the head's first column): the 32-column pieces from, from + step, ...
+// row and the head's first column): the 16-column pieces from, from + step, ...
 __device__ __forceinline__ void store_rows(__nv_bfloat16* out, int64_t ld, uint32_t t, int hd, float f,
                                            bool any, int live, int from, int step, uint8_t* stage, int lane) {
-  for (int c = from; c < (hd + 31) / 32; c += step) {
-    uint32_t o[32] = {};
+  for (int c = from; c < (hd + 15) / 16; c += step) {
+    uint32_t o[16] = {};
     if (any) {
-      tmem_ld32(t + c * 32, o);
+      tmem_ld16(t + c * 16, o);
       tmem_ld_wait();
     }
-    store_piece(out + c * 32, ld, o, f, hd - c * 32, live, smem_u32(stage), lane);
+    store_piece(out + c * 16, ld, o, f, hd - c * 16, live, smem_u32(stage), lane);
+  }
+}
+
+// Producer of both kernels (lane 0 of a warp that walks together): per piece of
+// work the fixed tiles, then the rings; `fixed` and `ring` issue the loads.
+template <int NC, class PieceT, class Fixed, class Ring>
+__device__ __forceinline__ void produce(const Smem<NC>& m, const AttnArgs& p, Work work, int lane, Fixed fixed,
+                                        Ring ring) {
+  using C = Cfg<NC>;
+  constexpr int ST = C::ST;
+  WorkQueue queue = m.queue();
+  int na = 0, nb = 0, loads = 0, asked = 0;
+  bool ok = true;
+  for (int pieces = 0;; ++pieces) {
+    if (lane == 0) {
+      const PieceT x(p, work);
+      if (x.steps > 0) {
+        ok = loads == 0 || mbar_wait(m.fix_empty, (loads - 1) & 1, m.abort_flag, p.err);
+        if (ok) {
+          mbar_arrive_expect_tx(m.fix_full, 2 * C::TILE);
+          fixed(x);
+          ++loads;
+        }
+        for (int n = 0; ok && n < x.steps; ++n) {
+          const int st = na % ST;
+          const uint32_t free = ((na / ST) & 1) ^ 1;
+          ok = mbar_wait(&m.a_empty[st], free, m.abort_flag, p.err);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&m.a_full[st], C::TILE);
+          ring(x, n, false, &m.a_full[st], m.ring_a + st * C::TILE);
+          ++na;
+          ok = mbar_wait(&m.b_empty[st], free, m.abort_flag, p.err);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&m.b_full[st], C::TILE);
+          ring(x, n, true, &m.b_full[st], m.ring_b + st * C::TILE);
+          ++nb;
+        }
+      }
+      // (only now: a block that asked early would hold a piece that an idle one could start)
+      ok = ok && queue.ask(pieces, m.abort_flag, p.err);
+      asked += ok;
+    }
+    __syncwarp();
+    if (!__all_sync(0xffffffffu, ok) || !queue.next(pieces, work, lane, m.abort_flag, p.err)) break;
+  }
+  if (lane == 0) {  // every copy has landed before the block may exit (at once, unless a wait ran out)
+    if (loads > 0) mbar_drain(m.fix_full, (loads - 1) & 1);
+    for (int n = max(0, na - ST); n < na; ++n) mbar_drain(&m.a_full[n % ST], (n / ST) & 1);
+    for (int n = max(0, nb - ST); n < nb; ++n) mbar_drain(&m.b_full[n % ST], (n / ST) & 1);
+    if (asked > 0) mbar_drain(&queue.full[(asked - 1) & 1], ((asked - 1) >> 1) & 1);
   }
 }
 
@@ -127,6 +185,23 @@ __device__ __forceinline__ void store_rows(__nv_bfloat16* out, int64_t ld, uint3
 // (bf16, 64), dQ.  Issue order: S(n + 1) once S(n) is read; then, once dS(n) is
 // written, dQ += dS(n) K(n) and dP(n + 1) -- whose arrival thus also says that
 // dS(n) has been read.
+struct DqPiece {
+  Seq sq;
+  int head, kv_head, i0, j0, steps;  // queries from i0 on, key blocks j0 .. j0 + steps - 1
+  bool live;
+
+  __device__ DqPiece(const AttnArgs& p, const Work& w) {
+    head = w.list % p.heads;
+    kv_head = head / p.group;
+    sq = seq_of(p, w.list / p.heads);
+    i0 = (static_cast<int>(gridDim.y) - 1 - w.block) * BT;  // longest rows first
+    live = i0 < sq.nq;
+    int j1;
+    key_blocks<BT, BT>(p, sq, i0, j0, j1);
+    steps = live ? j1 - j0 : 0;
+  }
+};
+
 template <int NC>
 __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     attn_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
@@ -140,12 +215,8 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
   const Smem<NC> m(smem_raw);  // fixed: Q, dO; rings: K, V
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int head = static_cast<int>(blockIdx.x % p.heads);
-  const Seq sq = seq_of(p, static_cast<int>(blockIdx.x / p.heads));
-  const int i0 = static_cast<int>(gridDim.y - 1 - blockIdx.y) * BT;  // longest rows first
-  if (i0 >= sq.nq) return;
-  int j0, j1;
-  key_blocks<BT, BT>(p, sq, i0, j0, j1);
+  Work work{static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y)};
+  WorkQueue queue = m.queue();
 
   if (threadIdx.x == 0) {
     Smem<NC>(smem_raw).init();
@@ -162,35 +233,21 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *m.tmem_slot;
-  const int kv_head = head / p.group;
-  const int steps = j1 - j0;
 
   if (warp < 4) {
     set_regs_dec<C::REGS_ISSUE>();
-    if (warp == 0 && lane == 0 && steps > 0) {
-      // ------------------------------------------------ TMA producer
-      const int row = static_cast<int>(sq.q0) + i0;
-      mbar_arrive_expect_tx(m.fix_full, 2 * C::TILE);
-      load_tile<NC>(&tmQ, m.fix_full, m.fix_a, head, row);
-      load_tile<NC>(&tmdO, m.fix_full, m.fix_b, head, row);
-      int na = 0, nb = 0;
-      for (int n = 0; n < steps; ++n) {
-        const int st = n % ST, krow = static_cast<int>(sq.k0) + (j0 + n) * BT;
-        const uint32_t free = ((n / ST) & 1) ^ 1;
-        if (!mbar_wait(&m.a_empty[st], free, m.abort_flag, p.err)) break;
-        mbar_arrive_expect_tx(&m.a_full[st], C::TILE);
-        load_tile<NC>(&tmK, &m.a_full[st], m.ring_a + st * C::TILE, kv_head, krow);
-        ++na;
-        if (!mbar_wait(&m.b_empty[st], free, m.abort_flag, p.err)) break;
-        mbar_arrive_expect_tx(&m.b_full[st], C::TILE);
-        load_tile<NC>(&tmV, &m.b_full[st], m.ring_b + st * C::TILE, kv_head, krow);
-        ++nb;
-      }
-      // every copy has landed before the block may exit (at once, unless a wait ran out)
-      mbar_drain(m.fix_full, 0);
-      for (int n = max(0, na - ST); n < na; ++n) mbar_drain(&m.a_full[n % ST], (n / ST) & 1);
-      for (int n = max(0, nb - ST); n < nb; ++n) mbar_drain(&m.b_full[n % ST], (n / ST) & 1);
-    } else if (warp == 1 && steps > 0) {
+    if (warp == 0) {
+      produce<NC, DqPiece>(
+          m, p, work, lane,
+          [&](const DqPiece& x) {
+            const int row = static_cast<int>(x.sq.q0) + x.i0;
+            load_tile<NC>(&tmQ, m.fix_full, m.fix_a, x.head, row);
+            load_tile<NC>(&tmdO, m.fix_full, m.fix_b, x.head, row);
+          },
+          [&](const DqPiece& x, int n, bool second, uint64_t* bar, uint8_t* dst) {
+            load_tile<NC>(second ? &tmV : &tmK, bar, dst, x.kv_head, static_cast<int>(x.sq.k0) + (x.j0 + n) * BT);
+          });
+    } else if (warp == 1) {
       // ------------------------------------------------ MMA issuer
       const int ks = (p.hd + 15) / 16;
       const uint32_t id_s = idesc_bf16(BT, BT, false, false);
@@ -200,43 +257,53 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       const uint64_t ring_a = kmajor_desc<BT>(m.ring_a), ring_b = kmajor_desc<BT>(m.ring_b);
       const uint64_t rows_a = rows_desc<BT>(m.ring_a);
       constexpr uint32_t STAGE = C::TILE >> 4;
-      bool ok = warp_wait(m.fix_full, 0, m.abort_flag, p.err);
-      auto scores = [&](int n) {  // S = Q K^T of block n
-        ok = ok && warp_wait(&m.a_full[n % ST], (n / ST) & 1, m.abort_flag, p.err);
-        if (!ok) return;
-        const int live = sq.nk - (j0 + n) * BT;
-        if (live < BT) clear_rows<NC>(m.ring_a + n % ST * C::TILE, BT, live, lane);
-        tc_fence_after();
-        product<NC, BT>(tmem, fix_a, ring_a + n % ST * STAGE, id_s, ks, issue);
-        mma_commit(m.s_full, issue);
-      };
-      auto dprobs = [&](int n) {  // dP = dO V^T of block n
-        ok = ok && warp_wait(&m.b_full[n % ST], (n / ST) & 1, m.abort_flag, p.err);
-        if (!ok) return;
-        const int live = sq.nk - (j0 + n) * BT;
-        if (live < BT) clear_rows<NC>(m.ring_b + n % ST * C::TILE, BT, live, lane);
-        tc_fence_after();
-        product<NC, BT>(tmem + T_DP, fix_b, ring_b + n % ST * STAGE, id_s, ks, issue);
-        mma_commit(m.dp_full, issue);
-        mma_commit(&m.b_empty[n % ST], issue);
-      };
-      scores(0);
-      dprobs(0);
-      for (int n = 0; ok && n < steps; ++n) {
-        if (n + 1 < steps) {
-          ok = warp_wait(m.s_read, n & 1, m.abort_flag, p.err);
-          scores(n + 1);
-        }
-        ok = ok && warp_wait(m.ds_full, n & 1, m.abort_flag, p.err);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t k = rows_a + n % ST * STAGE;
+      bool ok = true;
+      int base = 0, loads = 0;  // blocks and fixed tiles of the pieces before
+      for (int pieces = 0;; ++pieces) {
+        const DqPiece x(p, work);
+        // X = fixed streamed^T of block n
+        auto scores = [&](int n, uint64_t* full, uint8_t* ring, uint64_t b, uint64_t fix, uint32_t t, uint64_t* done) {
+          const int g = base + n, st = g % ST;
+          ok = ok && warp_wait(&full[st], (g / ST) & 1, m.abort_flag, p.err);
+          if (!ok) return;
+          const int rows = x.sq.nk - (x.j0 + n) * BT;
+          if (rows < BT) clear_rows<NC>(ring + st * C::TILE, BT, rows, lane);
+          tc_fence_after();
+          product<NC, BT>(tmem + t, fix, b + st * STAGE, id_s, ks, issue);
+          mma_commit(done, issue);
+        };
+        if (x.steps > 0) {
+          ok = warp_wait(m.fix_full, loads & 1, m.abort_flag, p.err);
+          ++loads;
+          scores(0, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+          scores(0, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
+          if (ok) mma_commit(&m.b_empty[base % ST], issue);
+          for (int n = 0; ok && n < x.steps; ++n) {
+            const int g = base + n;
+            const bool more = n + 1 < x.steps;
+            if (more) {
+              ok = warp_wait(m.s_read, g & 1, m.abort_flag, p.err);
+              scores(n + 1, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+            }
+            ok = ok && warp_wait(m.ds_full, g & 1, m.abort_flag, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t k = rows_a + g % ST * STAGE;
 #pragma unroll
-        for (int kk = 0; kk < BT / 16; ++kk)
-          mma_ts(tmem + T_DQ, tmem + T_DS + kk * 8, k + rows_step(kk), id_q, (kk > 0) | (n > 0), issue);
-        mma_commit(&m.a_empty[n % ST], issue);
-        if (n + 1 == steps) mma_commit(m.acc_full, issue);
-        if (n + 1 < steps) dprobs(n + 1);
+            for (int kk = 0; kk < BT / 16; ++kk)
+              mma_ts(tmem + T_DQ, tmem + T_DS + kk * 8, k + rows_step(kk), id_q, (kk > 0) | (n > 0), issue);
+            mma_commit(&m.a_empty[g % ST], issue);
+            if (more) {
+              scores(n + 1, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
+              if (ok) mma_commit(&m.b_empty[(g + 1) % ST], issue);
+            } else {
+              mma_commit(m.acc_full, issue);
+              mma_commit(m.fix_empty, issue);
+            }
+          }
+          base += x.steps;
+        }
+        if (!ok || !queue.next(pieces, work, lane, m.abort_flag, p.err)) break;
       }
       mma_commit(m.mma_done, issue);
       warp_wait(m.mma_done, 0, m.abort_flag, p.err);  // before tensor memory is freed
@@ -246,107 +313,115 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     // ------------------------------------------------ dS: a thread holds 32 keys of a query row
     const int w = (warp - 4) >> 2;
     const int quarter = warp & 3;  // tensor-memory lanes this warp may access
-    const int i = i0 + quarter * 32 + lane;
     const uint32_t t = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float c2 = p.scale * kAttnLog2e;
-    const int64_t at = sq.q0 + i;
-    int lo, hi;
-    keys_of(p, sq, i, lo, hi);
-    int full0, full1, unused;  // keys that every row of the tile sees
-    keys_of(p, sq, i0, unused, full1);
-    keys_of(p, sq, i0 + BT - 1, full0, unused);
-    float lse2 = 0.0f;
-    if (i < sq.nq) {
-      const float l = p.lse[head * p.Tq + at];
-      lse2 = l == -INFINITY ? 0.0f : l * kAttnLog2e;  // (no key: every place is masked below)
-    }
-    // delta = rowsum(dO * O): a warp takes 8 of the tile's rows, half a warp a row, all
-    // loads first; shared memory (and p_full, otherwise unused here) hands them round.
-    // (A thread per row, 16 bytes at a time, took 20,000 cycles.)
-    {
-      const int r0 = (warp - 4) * 8 + (lane >> 4), e = (lane & 15) * 8;
-      uint4 x[4], y[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[k] = y[k] = make_uint4(0, 0, 0, 0);
-        const int64_t row = sq.q0 + i0 + r0 + 2 * k;
-        if (i0 + r0 + 2 * k < sq.nq && e < p.hd) {
-          x[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.O) + row * p.ldo + head * p.hd + e));
-          y[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dO) + row * p.lddo + head * p.hd + e));
-        }
+    bool ok = true;
+    int base = 0, accs = 0;  // blocks of the pieces before, and pieces that had any
+    for (int pieces = 0;; ++pieces) {
+      const DqPiece x(p, work);
+      const int i = x.i0 + quarter * 32 + lane;
+      const int64_t at = x.sq.q0 + i;
+      int lo, hi;
+      keys_of(p, x.sq, i, lo, hi);
+      int full0, full1, unused;  // keys that every row of the tile sees
+      keys_of(p, x.sq, x.i0, unused, full1);
+      keys_of(p, x.sq, x.i0 + BT - 1, full0, unused);
+      float lse2 = 0.0f;
+      if (i < x.sq.nq) {
+        const float l = p.lse[x.head * p.Tq + at];
+        lse2 = l == -INFINITY ? 0.0f : l * kAttnLog2e;  // (no key: every place is masked below)
       }
+      // delta = rowsum(dO * O): a warp takes 8 of the tile's rows, half a warp a row, all
+      // loads first; shared memory (and p_full, otherwise unused here) hands them round.
+      // (A thread per row, 16 bytes at a time, took 20,000 cycles.)
+      {
+        const int r0 = (warp - 4) * 8 + (lane >> 4), e = (lane & 15) * 8;
+        uint4 o[4], d[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __nv_bfloat162* a = reinterpret_cast<const __nv_bfloat162*>(&x[k]);
-        const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&y[k]);
-        float sum = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 u = __bfloat1622float2(a[c]), v = __bfloat1622float2(b[c]);
-          sum = fmaf(u.x, v.x, fmaf(u.y, v.y, sum));
+        for (int k = 0; k < 4; ++k) {
+          o[k] = d[k] = make_uint4(0, 0, 0, 0);
+          const int64_t row = x.sq.q0 + x.i0 + r0 + 2 * k;
+          if (x.i0 + r0 + 2 * k < x.sq.nq && e < p.hd) {
+            o[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.O) + row * p.ldo + x.head * p.hd + e));
+            d[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dO) + row * p.lddo + x.head * p.hd + e));
+          }
         }
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const int r = r0 + 2 * k;
-        if ((lane & 15) == 0) {
-          m.rows[r] = sum;
-          if (i0 + r < sq.nq) p.delta[head * p.Tq + sq.q0 + i0 + r] = sum;  // for the other kernel
+        for (int k = 0; k < 4; ++k) {
+          const __nv_bfloat162* a = reinterpret_cast<const __nv_bfloat162*>(&o[k]);
+          const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&d[k]);
+          float sum = 0.0f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 u = __bfloat1622float2(a[c]), v = __bfloat1622float2(b[c]);
+            sum = fmaf(u.x, v.x, fmaf(u.y, v.y, sum));
+          }
+#pragma unroll
+          for (int b = 8; b > 0; b >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, b);
+          const int r = r0 + 2 * k;
+          if ((lane & 15) == 0) {
+            m.rows[r] = sum;
+            if (x.i0 + r < x.sq.nq) p.delta[x.head * p.Tq + x.sq.q0 + x.i0 + r] = sum;  // for the other kernel
+          }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(m.p_full);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(m.p_full);
-    }
-    bool ok = warp_wait(m.p_full, 0, m.abort_flag, p.err);
-    const float delta = m.rows[quarter * 32 + lane];
-    const float2 cc = make_float2(c2, c2), nl = make_float2(-lse2, -lse2), nd = make_float2(-delta, -delta);
-    const uint32_t count = static_cast<uint32_t>(hi - lo);
-    for (int n = 0; ok && n < steps; ++n) {
-      if (!warp_wait(m.s_full, n & 1, m.abort_flag, p.err)) { ok = false; break; }
+      ok = warp_wait(m.p_full, pieces & 1, m.abort_flag, p.err);
+      const float delta = m.rows[quarter * 32 + lane];
+      const float2 cc = make_float2(c2, c2), nl = make_float2(-lse2, -lse2), nd = make_float2(-delta, -delta);
+      const uint32_t count = static_cast<uint32_t>(hi - lo);
+      for (int n = 0; ok && n < x.steps; ++n) {
+        if (!warp_wait(m.s_full, (base + n) & 1, m.abort_flag, p.err)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t s[32];
+        tmem_ld32(t + w * 32, s);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(m.s_read);
+        const int key0 = (x.j0 + n) * BT;
+        if (key0 < full0 || key0 + BT > full1) {
+          const int a = lo - key0 - w * 32;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (static_cast<uint32_t>(k - a) >= count) s[k] = 0xff800000u;  // -inf
+        }
+        float2 pr[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float2 e = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), cc, nl);
+          pr[k] = make_float2(attn_exp2(e.x), attn_exp2(e.y));
+        }
+        if (!warp_wait(m.dp_full, (base + n) & 1, m.abort_flag, p.err)) { ok = false; break; }
+        tc_fence_after();
+        tmem_ld32(t + T_DP + w * 32, s);
+        tmem_ld_wait();
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float2 y = add2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), nd);
+          const float2 ds = mul2(pr[k], y);
+          pk[k] = pack2(ds.x, ds.y);
+        }
+        tmem_st16(t + T_DS + w * 16, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(m.ds_full);
+      }
+      if (ok && x.steps > 0) ok = warp_wait(m.acc_full, accs & 1, m.abort_flag, p.err);
+      accs += x.steps > 0;
+      base += x.steps;
       tc_fence_after();
-      uint32_t s[32];
-      tmem_ld32(t + w * 32, s);
-      tmem_ld_wait();
+      if (ok) {  // the warpgroups store a quarter of the row each
+        const int r0 = x.i0 + quarter * 32;
+        store_rows(static_cast<__nv_bfloat16*>(p.dQ) + (x.sq.q0 + r0) * p.lddq + x.head * p.hd, p.lddq, t + T_DQ, p.hd,
+                   p.scale, x.steps > 0, x.sq.nq - r0, w, C::GROUPS, m.out + (warp - 4) * 1024, lane);
+      }
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(m.s_read);
-      const int key0 = (j0 + n) * BT;
-      if (key0 < full0 || key0 + BT > full1) {
-        const int a = lo - key0 - w * 32;
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (static_cast<uint32_t>(k - a) >= count) s[k] = 0xff800000u;  // -inf
-      }
-      float2 pr[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float2 x = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), cc, nl);
-        pr[k] = make_float2(attn_exp2(x.x), attn_exp2(x.y));
-      }
-      if (!warp_wait(m.dp_full, n & 1, m.abort_flag, p.err)) { ok = false; break; }
-      tc_fence_after();
-      tmem_ld32(t + T_DP + w * 32, s);
-      tmem_ld_wait();
-      uint32_t pk[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float2 y = add2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), nd);
-        const float2 ds = mul2(pr[k], y);
-        pk[k] = pack2(ds.x, ds.y);
-      }
-      tmem_st16(t + T_DS + w * 16, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(m.ds_full);
+      if (!ok || !queue.next(pieces, work, lane, m.abort_flag, p.err)) break;
     }
-    if (ok && steps > 0) ok = warp_wait(m.acc_full, 0, m.abort_flag, p.err);
-    tc_fence_after();
-    if (ok) {  // the warpgroups store a quarter of the row each
-      const int r0 = i0 + quarter * 32;
-      store_rows(static_cast<__nv_bfloat16*>(p.dQ) + (sq.q0 + r0) * p.lddq + head * p.hd, p.lddq, t + T_DQ, p.hd,
-                 p.scale, steps > 0, sq.nq - r0, w, C::GROUPS, m.fix_a + (warp - 4) * 2048, lane);
-    }
-    tc_fence_before();
   }
   __syncthreads();
   if (warp == 1) {
@@ -363,6 +438,28 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
 // once P(n) is written; dK += dS^T(n) Q(n) and dP^T(n + 1) once dS(n) is.
 // Heads of more than 96 dims leave no columns for P^T: it then replaces S^T, and
 // S^T(n + 1) waits for dV's product (a separate P^T at head size 80: see below).
+struct DkvPiece {
+  Seq sq;
+  int kv_head, key0;       // keys from key0 on
+  int full0, full1;        // queries that see every key of the tile
+  int j0, nb, steps;       // step n: head n / nb of the group, query block j0 + n % nb
+  bool live;
+
+  __device__ DkvPiece(const AttnArgs& p, const Work& w) {
+    const int kv_heads = p.heads / p.group;
+    kv_head = w.list % kv_heads;
+    sq = seq_of(p, w.list / kv_heads);
+    key0 = w.block * BT;  // early keys are seen by most queries: first
+    live = key0 < sq.nk;
+    int qa, qb;  // queries that see some key of it
+    queries_of(p, sq, key0, qa, full1);
+    queries_of(p, sq, min(key0 + BT, sq.nk) - 1, full0, qb);
+    j0 = qa / BT;
+    nb = live && qb > qa ? (qb + BT - 1) / BT - j0 : 0;
+    steps = nb * p.group;
+  }
+};
+
 template <int NC>
 __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     attn_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
@@ -379,17 +476,8 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
   const Smem<NC> m(smem_raw);  // fixed: K, V; rings: Q, dO
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int kv_heads = p.heads / p.group;
-  const int kv_head = static_cast<int>(blockIdx.x % kv_heads);
-  const Seq sq = seq_of(p, static_cast<int>(blockIdx.x / kv_heads));
-  const int key0 = static_cast<int>(blockIdx.y) * BT;  // early keys are seen by most queries: first
-  if (key0 >= sq.nk) return;
-  // Queries [qa, qb) see some key of this tile, [full0, full1) every key of it.
-  int qa, qb, full0, full1;
-  queries_of(p, sq, key0, qa, full1);
-  queries_of(p, sq, min(key0 + BT, sq.nk) - 1, full0, qb);
-  const int j0 = qa / BT, nb = qb > qa ? (qb + BT - 1) / BT - j0 : 0;
-  const int steps = nb * p.group;  // step n: head n / nb of the group, block j0 + n % nb
+  Work work{static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y)};
+  WorkQueue queue = m.queue();
 
   if (threadIdx.x == 0) {
     Smem<NC>(smem_raw).init();
@@ -409,30 +497,19 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
 
   if (warp < 4) {
     set_regs_dec<C::REGS_ISSUE>();
-    if (warp == 0 && lane == 0 && steps > 0) {
-      // ------------------------------------------------ TMA producer
-      const int krow = static_cast<int>(sq.k0) + key0;
-      mbar_arrive_expect_tx(m.fix_full, 2 * C::TILE);
-      load_tile<NC>(&tmK, m.fix_full, m.fix_a, kv_head, krow);
-      load_tile<NC>(&tmV, m.fix_full, m.fix_b, kv_head, krow);
-      int na = 0, nb_ = 0;
-      for (int n = 0; n < steps; ++n) {
-        const int st = n % ST, head = kv_head * p.group + n / nb;
-        const int row = static_cast<int>(sq.q0) + (j0 + n % nb) * BT;
-        const uint32_t free = ((n / ST) & 1) ^ 1;
-        if (!mbar_wait(&m.a_empty[st], free, m.abort_flag, p.err)) break;
-        mbar_arrive_expect_tx(&m.a_full[st], C::TILE);
-        load_tile<NC>(&tmQ, &m.a_full[st], m.ring_a + st * C::TILE, head, row);
-        ++na;
-        if (!mbar_wait(&m.b_empty[st], free, m.abort_flag, p.err)) break;
-        mbar_arrive_expect_tx(&m.b_full[st], C::TILE);
-        load_tile<NC>(&tmdO, &m.b_full[st], m.ring_b + st * C::TILE, head, row);
-        ++nb_;
-      }
-      mbar_drain(m.fix_full, 0);
-      for (int n = max(0, na - ST); n < na; ++n) mbar_drain(&m.a_full[n % ST], (n / ST) & 1);
-      for (int n = max(0, nb_ - ST); n < nb_; ++n) mbar_drain(&m.b_full[n % ST], (n / ST) & 1);
-    } else if (warp == 1 && steps > 0) {
+    if (warp == 0) {
+      produce<NC, DkvPiece>(
+          m, p, work, lane,
+          [&](const DkvPiece& x) {
+            const int row = static_cast<int>(x.sq.k0) + x.key0;
+            load_tile<NC>(&tmK, m.fix_full, m.fix_a, x.kv_head, row);
+            load_tile<NC>(&tmV, m.fix_full, m.fix_b, x.kv_head, row);
+          },
+          [&](const DkvPiece& x, int n, bool second, uint64_t* bar, uint8_t* dst) {
+            load_tile<NC>(second ? &tmdO : &tmQ, bar, dst, x.kv_head * p.group + n / x.nb,
+                          static_cast<int>(x.sq.q0) + (x.j0 + n % x.nb) * BT);
+          });
+    } else if (warp == 1) {
       // ------------------------------------------------ MMA issuer
       const uint32_t id_s = idesc_bf16(BT, BT, false, false);
       const uint32_t id_a = idesc_bf16(BT, ks * 16, false, true);
@@ -441,45 +518,60 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       const uint64_t ring_a = kmajor_desc<BT>(m.ring_a), ring_b = kmajor_desc<BT>(m.ring_b);
       const uint64_t rows_a = rows_desc<BT>(m.ring_a), rows_b = rows_desc<BT>(m.ring_b);
       constexpr uint32_t STAGE = C::TILE >> 4;
-      bool ok = warp_wait(m.fix_full, 0, m.abort_flag, p.err);
-      // X^T = fixed streamed^T of step n
-      auto scores = [&](int n, uint64_t* full, uint8_t* ring, uint64_t b, uint64_t fix, uint32_t t, uint64_t* done) {
-        ok = ok && warp_wait(&full[n % ST], (n / ST) & 1, m.abort_flag, p.err);
-        if (!ok) return;
-        const int live = sq.nq - (j0 + n % nb) * BT;
-        if (live < BT) clear_rows<NC>(ring + n % ST * C::TILE, BT, live, lane);
-        tc_fence_after();
-        product<NC, BT>(tmem + t, fix, b + n % ST * STAGE, id_s, ks, issue);
-        mma_commit(done, issue);
-      };
-      // accumulator += (bf16 probabilities at t) . streamed rows of step n
-      auto add = [&](int n, uint64_t* ready, uint32_t t, uint32_t t_step, uint32_t acc, uint64_t rows,
-                     uint64_t* empty) {
-        ok = ok && warp_wait(ready, n & 1, m.abort_flag, p.err);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t b = rows + n % ST * STAGE;
+      bool ok = true;
+      int base = 0, loads = 0;  // steps and fixed tiles of the pieces before
+      for (int pieces = 0;; ++pieces) {
+        const DkvPiece x(p, work);
+        // X^T = fixed streamed^T of step n
+        auto scores = [&](int n, uint64_t* full, uint8_t* ring, uint64_t b, uint64_t fix, uint32_t t, uint64_t* done) {
+          const int g = base + n, st = g % ST;
+          ok = ok && warp_wait(&full[st], (g / ST) & 1, m.abort_flag, p.err);
+          if (!ok) return;
+          const int rows = x.sq.nq - (x.j0 + n % x.nb) * BT;
+          if (rows < BT) clear_rows<NC>(ring + st * C::TILE, BT, rows, lane);
+          tc_fence_after();
+          product<NC, BT>(tmem + t, fix, b + st * STAGE, id_s, ks, issue);
+          mma_commit(done, issue);
+        };
+        // accumulator += (bf16 probabilities at t) . streamed rows of step n
+        auto add = [&](int n, uint64_t* ready, uint32_t t, uint32_t t_step, uint32_t acc, uint64_t rows,
+                       uint64_t* empty) {
+          const int g = base + n;
+          ok = ok && warp_wait(ready, g & 1, m.abort_flag, p.err);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t b = rows + g % ST * STAGE;
 #pragma unroll
-        for (int kk = 0; kk < BT / 16; ++kk)
-          mma_ts(tmem + acc, tmem + t + (kk >> 1) * t_step + (kk & 1) * 8, b + rows_step(kk), id_a,
-                 (kk > 0) | (n > 0), issue);
-        mma_commit(&empty[n % ST], issue);
-      };
-      scores(0, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
-      scores(0, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
-      for (int n = 0; ok && n < steps; ++n) {
-        const bool more = n + 1 < steps;
-        if (apart && more) {
-          ok = warp_wait(m.s_read, n & 1, m.abort_flag, p.err);
-          scores(n + 1, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+          for (int kk = 0; kk < BT / 16; ++kk)
+            mma_ts(tmem + acc, tmem + t + (kk >> 1) * t_step + (kk & 1) * 8, b + rows_step(kk), id_a,
+                   (kk > 0) | (n > 0), issue);
+          mma_commit(&empty[g % ST], issue);
+        };
+        if (x.steps > 0) {
+          ok = warp_wait(m.fix_full, loads & 1, m.abort_flag, p.err);
+          ++loads;
+          scores(0, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+          scores(0, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
+          for (int n = 0; ok && n < x.steps; ++n) {
+            const bool more = n + 1 < x.steps;
+            if (apart && more) {
+              ok = warp_wait(m.s_read, (base + n) & 1, m.abort_flag, p.err);
+              scores(n + 1, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+            }
+            add(n, m.p_full, t_p, p_step, t_dv, rows_b, m.b_empty);
+            if (ok) mma_commit(m.p_free, issue);
+            if (!apart && more) scores(n + 1, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+            add(n, m.ds_full, T_DP, C::MC, t_dk, rows_a, m.a_empty);
+            if (more) scores(n + 1, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
+          }
+          if (ok) {
+            mma_commit(m.acc_full, issue);
+            mma_commit(m.fix_empty, issue);
+          }
+          base += x.steps;
         }
-        add(n, m.p_full, t_p, p_step, t_dv, rows_b, m.b_empty);
-        if (ok) mma_commit(m.p_free, issue);
-        if (!apart && more) scores(n + 1, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
-        add(n, m.ds_full, T_DP, C::MC, t_dk, rows_a, m.a_empty);
-        if (n + 1 < steps) scores(n + 1, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
+        if (!ok || !queue.next(pieces, work, lane, m.abort_flag, p.err)) break;
       }
-      if (ok) mma_commit(m.acc_full, issue);
       mma_commit(m.mma_done, issue);
       warp_wait(m.mma_done, 0, m.abort_flag, p.err);  // before tensor memory is freed
     }
@@ -492,104 +584,111 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t = tmem + lanes + w * 32;
     const float c2 = p.scale * kAttnLog2e;
-    int lo, hi;  // queries that see this thread's key
-    queries_of(p, sq, key0 + r, lo, hi);
-    const uint32_t count = static_cast<uint32_t>(hi - lo);
-    // lse and delta of the warp's 32 queries, a copy per warp: warps wait for nothing but
-    // their barriers; the next block's values are on their way while this one is worked on
-    float* buf = m.rows + (warp - 4) * 2 * C::MC;
-    float nl, nd;
-    auto fetch = [&](int n) {
-      const int head = kv_head * p.group + n / nb, i = (j0 + n % nb) * BT + w * 32 + lane;
-      nl = nd = 0.0f;
-      if (i < sq.nq) {
-        const int64_t at = head * p.Tq + sq.q0 + i;
-        const float l = p.lse[at];
-        nl = l == -INFINITY ? 0.0f : -l * kAttnLog2e;  // (no key: every place is masked below)
-        nd = -p.delta[at];
-      }
-    };
-    if (steps > 0) fetch(0);
-    const float2 cc = make_float2(c2, c2);
     bool ok = true;
-    for (int n = 0; n < steps; ++n) {
-      const int i0 = (j0 + n % nb) * BT;
-      __syncwarp();  // the previous block's values are read
-      buf[lane] = nl;
-      buf[C::MC + lane] = nd;
-      __syncwarp();
-      if (n + 1 < steps) fetch(n + 1);
-      if (!warp_wait(m.s_full, n & 1, m.abort_flag, p.err)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t s[32], pk[16];
-      tmem_ld32(t, s);
-      tmem_ld_wait();
-      if (apart) {
+    int base = 0, accs = 0;  // steps of the pieces before, and pieces that had any
+    for (int pieces = 0;; ++pieces) {
+      const DkvPiece x(p, work);
+      int lo, hi;  // queries that see this thread's key
+      queries_of(p, x.sq, x.key0 + r, lo, hi);
+      const uint32_t count = static_cast<uint32_t>(hi - lo);
+      // lse and delta of the warp's 32 queries, a copy per warp: warps wait for nothing but
+      // their barriers; the next block's values are on their way while this one is worked on
+      float* buf = m.rows + (warp - 4) * 2 * C::MC;
+      float nl, nd;
+      auto fetch = [&](int n) {
+        const int head = x.kv_head * p.group + n / x.nb, i = (x.j0 + n % x.nb) * BT + w * 32 + lane;
+        nl = nd = 0.0f;
+        if (i < x.sq.nq) {
+          const int64_t at = head * p.Tq + x.sq.q0 + i;
+          const float l = p.lse[at];
+          nl = l == -INFINITY ? 0.0f : -l * kAttnLog2e;  // (no key: every place is masked below)
+          nd = -p.delta[at];
+        }
+      };
+      if (x.steps > 0) fetch(0);
+      const float2 cc = make_float2(c2, c2);
+      for (int n = 0; ok && n < x.steps; ++n) {
+        const int i0 = (x.j0 + n % x.nb) * BT;
+        __syncwarp();  // the previous block's values are read
+        buf[lane] = nl;
+        buf[C::MC + lane] = nd;
+        __syncwarp();
+        if (n + 1 < x.steps) fetch(n + 1);
+        if (!warp_wait(m.s_full, (base + n) & 1, m.abort_flag, p.err)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t s[32], pk[16];
+        tmem_ld32(t, s);
+        tmem_ld_wait();
+        if (apart) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(m.s_read);
+        }
+        if (i0 < x.full0 || i0 + BT > x.full1) {
+          const int a = lo - i0 - w * 32;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (static_cast<uint32_t>(k - a) >= count) s[k] = 0xff800000u;  // -inf
+        }
+        float2 pr[16];
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          const float4 l = *reinterpret_cast<const float4*>(buf + 2 * k);
+          const float2 u = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), cc,
+                                make_float2(l.x, l.y));
+          const float2 v = fma2(make_float2(__uint_as_float(s[2 * k + 2]), __uint_as_float(s[2 * k + 3])), cc,
+                                make_float2(l.z, l.w));
+          pr[k] = make_float2(attn_exp2(u.x), attn_exp2(u.y));
+          pr[k + 1] = make_float2(attn_exp2(v.x), attn_exp2(v.y));
+          pk[k] = pack2(pr[k].x, pr[k].y);
+          pk[k + 1] = pack2(pr[k + 1].x, pr[k + 1].y);
+        }
+        // (P of the block before has been multiplied long since)
+        if (base + n > 0 && !warp_wait(m.p_free, (base + n - 1) & 1, m.abort_flag, p.err)) { ok = false; break; }
+        tc_fence_after();
+        tmem_st16(tmem + lanes + t_p + w * p_step, pk);
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(m.s_read);
-      }
-      if (i0 < full0 || i0 + BT > full1) {
-        const int a = lo - i0 - w * 32;
+        if (lane == 0) mbar_arrive(m.p_full);
+        if (!warp_wait(m.dp_full, (base + n) & 1, m.abort_flag, p.err)) { ok = false; break; }
+        tc_fence_after();
+        tmem_ld32(t + T_DP, s);
+        tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (static_cast<uint32_t>(k - a) >= count) s[k] = 0xff800000u;  // -inf
+        for (int k = 0; k < 16; k += 2) {
+          const float4 d = *reinterpret_cast<const float4*>(buf + C::MC + 2 * k);
+          const float2 u = mul2(pr[k], add2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])),
+                                            make_float2(d.x, d.y)));
+          const float2 v = mul2(pr[k + 1], add2(make_float2(__uint_as_float(s[2 * k + 2]), __uint_as_float(s[2 * k + 3])),
+                                                make_float2(d.z, d.w)));
+          pk[k] = pack2(u.x, u.y);
+          pk[k + 1] = pack2(v.x, v.y);
+        }
+        tmem_st16(t + T_DP, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(m.ds_full);
       }
-      float2 pr[16];
-#pragma unroll
-      for (int k = 0; k < 16; k += 2) {
-        const float4 l = *reinterpret_cast<const float4*>(buf + 2 * k);
-        const float2 x = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), cc,
-                              make_float2(l.x, l.y));
-        const float2 y = fma2(make_float2(__uint_as_float(s[2 * k + 2]), __uint_as_float(s[2 * k + 3])), cc,
-                              make_float2(l.z, l.w));
-        pr[k] = make_float2(attn_exp2(x.x), attn_exp2(x.y));
-        pr[k + 1] = make_float2(attn_exp2(y.x), attn_exp2(y.y));
-        pk[k] = pack2(pr[k].x, pr[k].y);
-        pk[k + 1] = pack2(pr[k + 1].x, pr[k + 1].y);
-      }
-      // (P of the block before has been multiplied long since)
-      if (n > 0 && !warp_wait(m.p_free, (n - 1) & 1, m.abort_flag, p.err)) { ok = false; break; }
+      if (ok && x.steps > 0) ok = warp_wait(m.acc_full, accs & 1, m.abort_flag, p.err);
+      accs += x.steps > 0;
+      base += x.steps;
       tc_fence_after();
-      tmem_st16(tmem + lanes + t_p + w * p_step, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(m.p_full);
-      if (!warp_wait(m.dp_full, n & 1, m.abort_flag, p.err)) { ok = false; break; }
-      tc_fence_after();
-      tmem_ld32(t + T_DP, s);
-      tmem_ld_wait();
-#pragma unroll
-      for (int k = 0; k < 16; k += 2) {
-        const float4 d = *reinterpret_cast<const float4*>(buf + C::MC + 2 * k);
-        const float2 x = mul2(pr[k], add2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])),
-                                          make_float2(d.x, d.y)));
-        const float2 y = mul2(pr[k + 1], add2(make_float2(__uint_as_float(s[2 * k + 2]), __uint_as_float(s[2 * k + 3])),
-                                              make_float2(d.z, d.w)));
-        pk[k] = pack2(x.x, x.y);
-        pk[k + 1] = pack2(y.x, y.y);
+      if (ok) {  // the even warpgroups write dV, the odd ones dK, half a row each
+        const int r0 = x.key0 + quarter * 32;
+        const int64_t at = x.sq.k0 + r0;
+        uint8_t* stage = m.out + (warp - 4) * 1024;
+        if ((w & 1) == 0)
+          store_rows(static_cast<__nv_bfloat16*>(p.dV) + at * p.lddv + x.kv_head * p.hd, p.lddv, tmem + lanes + t_dv, p.hd,
+                     1.0f, x.steps > 0, x.sq.nk - r0, w >> 1, 2, stage, lane);
+        else
+          store_rows(static_cast<__nv_bfloat16*>(p.dK) + at * p.lddk + x.kv_head * p.hd, p.lddk, tmem + lanes + t_dk, p.hd,
+                     p.scale, x.steps > 0, x.sq.nk - r0, w >> 1, 2, stage, lane);
       }
-      tmem_st16(t + T_DP, pk);
-      tmem_st_wait();
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(m.ds_full);
+      if (!ok || !queue.next(pieces, work, lane, m.abort_flag, p.err)) break;
     }
-    if (ok && steps > 0) ok = warp_wait(m.acc_full, 0, m.abort_flag, p.err);
-    tc_fence_after();
-    if (ok) {  // the even warpgroups write dV, the odd ones dK, half a row each
-      const int r0 = key0 + quarter * 32;
-      const int64_t at = sq.k0 + r0;
-      uint8_t* stage = m.fix_a + (warp - 4) * 2048;
-      if ((w & 1) == 0)
-        store_rows(static_cast<__nv_bfloat16*>(p.dV) + at * p.lddv + kv_head * p.hd, p.lddv, tmem + lanes + t_dv, p.hd,
-                   1.0f, steps > 0, sq.nk - r0, w >> 1, 2, stage, lane);
-      else
-        store_rows(static_cast<__nv_bfloat16*>(p.dK) + at * p.lddk + kv_head * p.hd, p.lddk, tmem + lanes + t_dk, p.hd,
-                   p.scale, steps > 0, sq.nk - r0, w >> 1, 2, stage, lane);
-    }
-    tc_fence_before();
   }
   __syncthreads();
   if (warp == 1) {

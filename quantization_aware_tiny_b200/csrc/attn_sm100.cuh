@@ -287,17 +287,19 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int rows, int from, in
   __syncwarp();
 }
 
-// bf16(v * f) of 32 accumulator columns of the warp's 32 rows (a row per lane) to
-// global rows ld apart, columns [0, cols) of the piece and rows [0, live): through
-// 2 KiB of shared memory, so that a store instruction covers 8 rows of 64 bytes.
-// (Each lane storing its own row in 16-byte pieces took 3,700 cycles for dK and dV
-// of a 128-key tile.)
-__device__ __forceinline__ void store_piece(__nv_bfloat16* out, int64_t ld, const uint32_t (&v)[32],
+// bf16(v * f) of N (16 or 32) accumulator columns of the warp's 32 rows (a row per
+// lane) to global rows ld apart, columns [0, cols) of the piece and rows [0, live):
+// through 64 N bytes of shared memory, so that a store instruction covers whole
+// sectors of several rows.  (Each lane storing its own row in 16-byte pieces took
+// 3,700 cycles for dK and dV of a 128-key tile.)
+template <int N>
+__device__ __forceinline__ void store_piece(__nv_bfloat16* out, int64_t ld, const uint32_t (&v)[N],
                                             float f, int cols, int live, uint32_t stage, int lane) {
-  const uint32_t mine = stage + lane * 64;
-  const int sw = (lane >> 1) & 3;
+  constexpr int G = N / 8;  // 16-byte groups of a row
+  const uint32_t mine = stage + lane * 2 * N;
+  const int sw = (lane * G >> 3) & (G - 1);  // keeps 8 neighbouring lanes off one another's banks
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
+  for (int g = 0; g < G; ++g) {
     uint32_t o[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -305,11 +307,11 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16* out, int64_t ld, cons
     st_shared_v4(mine + ((g ^ sw) << 4), o[0], o[1], o[2], o[3]);
   }
   __syncwarp();
-  const int g = lane & 3;
+  const int g = lane & (G - 1);
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const int r = n * 8 + (lane >> 2);
-    const uint4 x = ld_shared_v4(stage + r * 64 + ((g ^ ((r >> 1) & 3)) << 4));
+  for (int n = 0; n < G; ++n) {
+    const int r = n * (32 / G) + lane / G;
+    const uint4 x = ld_shared_v4(stage + r * 2 * N + ((g ^ ((r * G >> 3) & (G - 1))) << 4));
     if (r < live && g * 8 < cols) *reinterpret_cast<uint4*>(out + r * ld + g * 8) = x;
   }
   __syncwarp();

@@ -215,6 +215,15 @@ def test_bwd_queries_and_keys_of_other_lengths(lens, mask):
     Case(*lens, heads=2, kv_heads=2, hd=80, **mask).check_backward()
 
 
+def test_bwd_more_pieces_than_the_gpu_holds():
+    g = torch.Generator().manual_seed(0)
+    lens = torch.randint(0, 400, (300,), generator=g).tolist()
+    Case(lens, heads=4, kv_heads=2, hd=16).check_backward()
+    lq = torch.randint(0, 65, (700,), generator=g).tolist()
+    lk = torch.randint(0, 300, (700,), generator=g).tolist()
+    Case(lq, lk, heads=4, kv_heads=2, hd=104).check_backward()
+
+
 def test_bwd_equal_lengths_without_tables():
     Case([160] * 3, packed=False).check_backward()
     Case([64] * 3, [200] * 3, packed=False, hd=128).check_backward()
