@@ -442,7 +442,7 @@ struct DkvPiece {
   Seq sq;
   int kv_head, key0;       // keys from key0 on
   int full0, full1;        // queries that see every key of the tile
-  int j0, nb, steps;       // step n: head n / nb of the group, query block j0 + n % nb
+  int j0, nb, steps;       // the steps: query blocks j0 .. j0 + nb - 1 of each head of the group
   bool live;
 
   __device__ DkvPiece(const AttnArgs& p, const Work& w) {
@@ -457,6 +457,18 @@ struct DkvPiece {
     j0 = qa / BT;
     nb = live && qb > qa ? (qb + BT - 1) / BT - j0 : 0;
     steps = nb * p.group;
+  }
+};
+
+// Head (within the group) and block of a step, counted along: divided out of the
+// step's number by the one issuing warp they cost 800 of a step's 3,500 cycles.
+struct Step {
+  int head = 0, block = 0;
+  __device__ void advance(int nb) {
+    if (++block == nb) {
+      block = 0;
+      ++head;
+    }
   }
 };
 
@@ -498,6 +510,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
   if (warp < 4) {
     set_regs_dec<C::REGS_ISSUE>();
     if (warp == 0) {
+      Step at;
       produce<NC, DkvPiece>(
           m, p, work, lane,
           [&](const DkvPiece& x) {
@@ -506,8 +519,10 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
             load_tile<NC>(&tmV, m.fix_full, m.fix_b, x.kv_head, row);
           },
           [&](const DkvPiece& x, int n, bool second, uint64_t* bar, uint8_t* dst) {
-            load_tile<NC>(second ? &tmdO : &tmQ, bar, dst, x.kv_head * p.group + n / x.nb,
-                          static_cast<int>(x.sq.q0) + (x.j0 + n % x.nb) * BT);
+            if (n == 0) at = Step();
+            load_tile<NC>(second ? &tmdO : &tmQ, bar, dst, x.kv_head * p.group + at.head,
+                          static_cast<int>(x.sq.q0) + (x.j0 + at.block) * BT);
+            if (second) at.advance(x.nb);
           });
     } else if (warp == 1) {
       // ------------------------------------------------ MMA issuer
@@ -522,12 +537,15 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       int base = 0, loads = 0;  // steps and fixed tiles of the pieces before
       for (int pieces = 0;; ++pieces) {
         const DkvPiece x(p, work);
+        const int tail = x.sq.nq - x.j0 * BT;  // rows from the first block on
+        Step at_s, at_dp;                      // of the next S^T and dP^T
         // X^T = fixed streamed^T of step n
-        auto scores = [&](int n, uint64_t* full, uint8_t* ring, uint64_t b, uint64_t fix, uint32_t t, uint64_t* done) {
+        auto scores = [&](int n, Step& at, uint64_t* full, uint8_t* ring, uint64_t b, uint64_t fix, uint32_t t, uint64_t* done) {
           const int g = base + n, st = g % ST;
           ok = ok && warp_wait(&full[st], (g / ST) & 1, m.abort_flag, p.err);
           if (!ok) return;
-          const int rows = x.sq.nq - (x.j0 + n % x.nb) * BT;
+          const int rows = tail - at.block * BT;
+          at.advance(x.nb);
           if (rows < BT) clear_rows<NC>(ring + st * C::TILE, BT, rows, lane);
           tc_fence_after();
           product<NC, BT>(tmem + t, fix, b + st * STAGE, id_s, ks, issue);
@@ -550,19 +568,19 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
         if (x.steps > 0) {
           ok = warp_wait(m.fix_full, loads & 1, m.abort_flag, p.err);
           ++loads;
-          scores(0, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
-          scores(0, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
+          scores(0, at_s, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+          scores(0, at_dp, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
           for (int n = 0; ok && n < x.steps; ++n) {
             const bool more = n + 1 < x.steps;
             if (apart && more) {
               ok = warp_wait(m.s_read, (base + n) & 1, m.abort_flag, p.err);
-              scores(n + 1, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+              scores(n + 1, at_s, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
             }
             add(n, m.p_full, t_p, p_step, t_dv, rows_b, m.b_empty);
             if (ok) mma_commit(m.p_free, issue);
-            if (!apart && more) scores(n + 1, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
+            if (!apart && more) scores(n + 1, at_s, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
             add(n, m.ds_full, T_DP, C::MC, t_dk, rows_a, m.a_empty);
-            if (more) scores(n + 1, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
+            if (more) scores(n + 1, at_dp, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
           }
           if (ok) {
             mma_commit(m.acc_full, issue);
@@ -594,26 +612,31 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       // lse and delta of the warp's 32 queries, a copy per warp: warps wait for nothing but
       // their barriers; the next block's values are on their way while this one is worked on
       float* buf = m.rows + (warp - 4) * 2 * C::MC;
-      float nl, nd;
-      auto fetch = [&](int n) {
-        const int head = x.kv_head * p.group + n / x.nb, i = (x.j0 + n % x.nb) * BT + w * 32 + lane;
-        nl = nd = 0.0f;
+      float l = 0.0f, d = 0.0f;  // as loaded: nothing waits for them before the next block
+      Step next;  // of the next fetch
+      auto fetch = [&]() {
+        const int i = (x.j0 + next.block) * BT + w * 32 + lane;
         if (i < x.sq.nq) {
-          const int64_t at = head * p.Tq + x.sq.q0 + i;
-          const float l = p.lse[at];
-          nl = l == -INFINITY ? 0.0f : -l * kAttnLog2e;  // (no key: every place is masked below)
-          nd = -p.delta[at];
+          const int64_t at = (x.kv_head * p.group + next.head) * p.Tq + x.sq.q0 + i;
+          l = p.lse[at];
+          d = p.delta[at];
         }
+        next.advance(x.nb);
       };
-      if (x.steps > 0) fetch(0);
+      if (x.steps > 0) fetch();
+      int block = 0;  // of the step
       const float2 cc = make_float2(c2, c2);
       for (int n = 0; ok && n < x.steps; ++n) {
-        const int i0 = (x.j0 + n % x.nb) * BT;
+        const int i0 = (x.j0 + block) * BT;
+        if (++block == x.nb) block = 0;
         __syncwarp();  // the previous block's values are read
-        buf[lane] = nl;
-        buf[C::MC + lane] = nd;
+        // (behind the last query the rows are cleared, whatever lse and delta hold there;
+        // lse = -inf, no key: every place is masked below)
+        const bool there = i0 + w * 32 + lane < x.sq.nq;
+        buf[lane] = there && l != -INFINITY ? -l * kAttnLog2e : 0.0f;
+        buf[C::MC + lane] = there ? -d : 0.0f;
         __syncwarp();
-        if (n + 1 < x.steps) fetch(n + 1);
+        if (n + 1 < x.steps) fetch();
         if (!warp_wait(m.s_full, (base + n) & 1, m.abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[32], pk[16];
