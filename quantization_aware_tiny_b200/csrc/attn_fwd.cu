@@ -93,11 +93,13 @@ struct Piece {
     if (!live) j1 = j0;
   }
   static constexpr int STEP = SHORT ? 2 : 1;
+  __device__ int from(int w) const { return w ? b0[1] : b0[0]; }
+  __device__ int to(int w) const { return w ? b1[1] : b1[0]; }
   __device__ bool has(int w, int j) const {
-    return j >= b0[w] && j < b1[w] && (!SHORT || ((j - b0[w]) & 1) == 0);
+    return j >= from(w) && j < to(w) && (!SHORT || ((j - from(w)) & 1) == 0);
   }
-  __device__ bool any(int w) const { return b0[w] < b1[w]; }
-  __device__ bool last(int w, int j) const { return j + STEP >= b1[w]; }
+  __device__ bool any(int w) const { return from(w) < to(w); }
+  __device__ bool last(int w, int j) const { return j + STEP >= to(w); }
 };
 
 template <int NC, bool SHORT>
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
                 const int rows = x.sq.nk - (j - 1) * BKV;
                 if (rows < BKV) clear_rows<NC>(sV + pst * C::TILE, BKV, rows, lane);
                 tc_fence_after();
-                const uint32_t more = j - 1 > x.b0[w];
+                const uint32_t more = j - 1 > x.from(w);
 #pragma unroll
                 for (int kk = 0; kk < BKV / 16; ++kk)
                   mma_ts(tmem + 256 + w * C::O_COLS, tmem + w * 128 + kk * 8,
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     const uint32_t stage = smem_u32(sOut) + (warp - 4) * 2048;
     const int ocols = (p.hd + 31) / 32;
     const float c2 = p.scale * kAttnLog2e;
-    uint32_t ph = 0, oph[2] = {0, 0}, mph = 0;
+    uint32_t ph = 0, oph = 0, oph1 = 0, mph = 0;  // oph: the own tile's O, oph1: SHORT, tile 1's
     bool ok = true;
     for (int pieces = 0;; ++pieces) {
       const Piece<SHORT> x(p, work);
@@ -324,7 +326,8 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
         ok = warp_wait(m_empty, mph, abort_flag, p.err);
         mph ^= 1u;
       }
-      for (int j = x.b0[w]; ok && j < x.b1[w]; j += x.STEP) {
+      const int from = x.from(w), to = x.to(w);
+      for (int j = from; ok && j < to; j += x.STEP) {
         if (!warp_wait(&s_full[w], ph, abort_flag, p.err)) { ok = false; break; }
         ph ^= 1u;
         tc_fence_after();
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
         const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const bool grow = (mb - m) * c2 > C::RESCALE || m == -INFINITY;
         const float mn = grow ? fmaxf(m, mb) : m;
-        if (j > x.b0[w] && __any_sync(0xffffffffu, mn > m && m != -INFINITY)) {
+        if (j > from && __any_sync(0xffffffffu, mn > m && m != -INFINITY)) {
           // S complete implies every earlier product is: O may be read and written
           const float f = mn > m ? attn_exp2((m - mn) * c2) : 1.0f;
           l *= f;
@@ -408,13 +411,13 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
           f1 = other.x == -INFINITY ? 0.0f : attn_exp2((other.x - top) * c2);
           l = l * f0 + other.y * f1;
           m = top;
-          if (ok && any1) ok = warp_wait(&o_full[1], oph[1], abort_flag, p.err);
-          if (any1) oph[1] ^= 1u;
+          if (ok && any1) ok = warp_wait(&o_full[1], oph1, abort_flag, p.err);
+          if (any1) oph1 ^= 1u;
         }
       }
       if (!SHORT || w == 0) {
-        if (ok && any0) ok = warp_wait(&o_full[w], oph[w], abort_flag, p.err);
-        if (any0) oph[w] ^= 1u;
+        if (ok && any0) ok = warp_wait(&o_full[w], oph, abort_flag, p.err);
+        if (any0) oph ^= 1u;
       }
       tc_fence_after();
       if (rows && ok) {
