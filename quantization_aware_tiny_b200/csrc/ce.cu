@@ -11,7 +11,7 @@ namespace qat {
 namespace {
 
 constexpr int kJoinRows = 32;   // tokens of a block: one per lane, so the pairs load coalesced
-constexpr int kJoinWarps = 8;   // slots are dealt to the warps in turn
+constexpr int kJoinWarps = 32;  // most warps of a block; slots are dealt to them in turn
 
 // (sum of losses, counted tokens) of a block of kJoinRows tokens.
 struct alignas(16) CePart {
@@ -31,13 +31,14 @@ __device__ __forceinline__ void merge_stats(float& m, float& s, float m2, float 
 // lse = m + log s, loss = lse - logit of the target (0 without one).  Bound by
 // reading slots * T pairs: 33.5 MB for 65,536 tokens of 8,192 words.
 __global__ void __launch_bounds__(kJoinRows* kJoinWarps) ce_join_kernel(const CeJoin j) {
+  const int warps = blockDim.x >> 5;
   __shared__ float2 part[kJoinWarps][kJoinRows];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kJoinRows + lane;
   float m = -INFINITY, s = 0.0f;
   if (t < j.T) {
 #pragma unroll 4
-    for (int i = w; i < j.slots; i += kJoinWarps) {
+    for (int i = w; i < j.slots; i += warps) {
       const float2 v = j.stats[static_cast<int64_t>(i) * j.T + t];
       merge_stats(m, s, v.x, v.y);
     }
@@ -45,8 +46,7 @@ __global__ void __launch_bounds__(kJoinRows* kJoinWarps) ce_join_kernel(const Ce
   part[w][lane] = make_float2(m, s);
   __syncthreads();
   if (w != 0) return;
-#pragma unroll
-  for (int i = 1; i < kJoinWarps; ++i) merge_stats(m, s, part[i][lane].x, part[i][lane].y);
+  for (int i = 1; i < warps; ++i) merge_stats(m, s, part[i][lane].x, part[i][lane].y);
   double sum = 0.0;
   int count = 0;
   if (t < j.T) {
@@ -115,7 +115,10 @@ int64_t ce_parts_bytes(int64_t T) { return join_blocks(T) * static_cast<int64_t>
 
 int launch_ce_join(const CeJoin& j, cudaStream_t stream) {
   const int64_t blocks = join_blocks(j.T);
-  ce_join_kernel<<<static_cast<unsigned>(blocks), kJoinRows * kJoinWarps, 0, stream>>>(j);
+  // about 8 slots a warp: 64 slots (8,192 words) 8 warps, 394 (50,257 words) 32, where 8
+  // warps took 25 us for 4,099 tokens
+  const int warps = std::min(kJoinWarps, std::max(1, (j.slots + 7) / 8));
+  ce_join_kernel<<<static_cast<unsigned>(blocks), kJoinRows * warps, 0, stream>>>(j);
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return QAT_ERR_CUDA;

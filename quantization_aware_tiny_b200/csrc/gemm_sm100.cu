@@ -153,38 +153,68 @@ __device__ __forceinline__ void ce_stats_chunk(const KArgs& p, uint32_t (&acc)[3
   for (int j = 4; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
   const float m = fmaxf(c.m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
   const float m2 = m * kLog2e;
-  float sum[4] = {c.s * exp2_fast(fmaf(c.m, kLog2e, -m2)), 0.0f, 0.0f, 0.0f};
+  const float2 l2 = make_float2(kLog2e, kLog2e), nm = make_float2(-m2, -m2);
+  float2 sum[2] = {make_float2(c.s * exp2_fast(fmaf(c.m, kLog2e, -m2)), 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-  for (int j = 0; j < 32; ++j) sum[j & 3] += exp2_fast(fmaf(v[j], kLog2e, -m2));
-  c.m = m;
-  c.s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-}
-
-// Gradient of one 32-column chunk in place: acc <- (softmax - [target]) * scale.
-__device__ __forceinline__ void ce_grad_chunk(const KArgs& p, uint32_t (&acc)[32], int col0,
-                                              int row, const CeRow& c) {
-  float* v = reinterpret_cast<float*>(acc);
-#pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = exp2_fast(fmaf(v[j], kLog2e, -c.lse2));
-  const int idx = c.target - col0;
-  const bool here = c.target >= 0 && idx >= 0 && idx < 32;
-  if (__any_sync(0xffffffffu, here)) {
-    float t = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      v[j] -= (here && j == idx) ? 1.0f : 0.0f;
-      t = (j == idx) ? v[j] : t;
-    }
-    t *= c.scale;
-    if (here && p.ce.rem) p.ce.rem[row] = t - bf2f(__float2bfloat16_rn(t));
+  for (int j = 0; j < 32; j += 2) {
+    const float2 x = fma2(make_float2(v[j], v[j + 1]), l2, nm);
+    sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], make_float2(exp2_fast(x.x), exp2_fast(x.y)));
   }
-#pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] *= c.scale;
+  const float2 both = add2(sum[0], sum[1]);
+  c.m = m;
+  c.s = both.x + both.y;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 v = __floats2bfloat162_rn(a, b);  // .x = a (low half), .y = b
   return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Gradient of one 32-column chunk, g = (softmax - [target]) * scale, staged as
+// bf16(g) in buf0 and, with keep_lo, bf16(g - bf16(g)) in buf1 (32 rows x 64 B,
+// swizzled as stage_chunk does), two columns an instruction.
+__device__ __forceinline__ void stage_grad_chunk(const KArgs& p, const uint32_t (&acc)[32], int col0,
+                                                 int row, const CeRow& c, uint32_t buf0, uint32_t buf1,
+                                                 bool keep_lo, int lane) {
+  const float* a = reinterpret_cast<const float*>(acc);
+  const float2 l2 = make_float2(kLog2e, kLog2e), nl = make_float2(-c.lse2, -c.lse2);
+  const float2 sc = make_float2(c.scale, c.scale);
+  float2 v[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float2 x = fma2(make_float2(a[2 * k], a[2 * k + 1]), l2, nl);
+    v[k] = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+  }
+  const int idx = c.target - col0;
+  const bool here = c.target >= 0 && idx >= 0 && idx < 32;
+  if (__any_sync(0xffffffffu, here)) {  // some row's target lies in this chunk
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      v[k].x -= (here && 2 * k == idx) ? 1.0f : 0.0f;
+      v[k].y -= (here && 2 * k + 1 == idx) ? 1.0f : 0.0f;
+      t = 2 * k == idx ? v[k].x : 2 * k + 1 == idx ? v[k].y : t;
+    }
+    t *= c.scale;
+    if (here && p.ce.rem) p.ce.rem[row] = t - bf2f(__float2bfloat16_rn(t));
+  }
+  const uint32_t off = static_cast<uint32_t>(lane) * 64u;
+  const int sw = (lane >> 1) & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 g = mul2(v[4 * j + k], sc);
+      hi[k] = pack_bf16(g.x, g.y);
+      const float2 back = make_float2(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xffff0000u));
+      const float2 rest = fma2(back, make_float2(-1.0f, -1.0f), g);
+      lo[k] = pack_bf16(rest.x, rest.y);
+    }
+    const uint32_t at = off + (static_cast<uint32_t>(j ^ sw) << 4);
+    st_shared_v4(buf0 + at, hi[0], hi[1], hi[2], hi[3]);
+    if (keep_lo) st_shared_v4(buf1 + at, lo[0], lo[1], lo[2], lo[3]);
+  }
 }
 
 // Epilogue of one 32-column chunk of one row (this lane's), staged into the
@@ -226,8 +256,6 @@ __device__ __forceinline__ void stage_chunk(const KArgs& p, const uint32_t (&acc
           // d/dx leaky(x, 0.5)^2 = 2x (x > 0), x/2 (x <= 0): the scalings are exact
           const float pre = bf2f(r[i]);
           o[i] = __fmul_rn(a, pre > 0.0f ? __fmul_rn(pre, 2.0f) : __fmul_rn(pre, 0.5f));
-        } else if constexpr (EPI == EPI_CE_GRAD) {  // buf0 <- bf16(g), buf1 <- bf16(g - bf16(g))
-          o[i] = __fsub_rn(a, bf2f(__float2bfloat16_rn(a)));
         } else if constexpr (EPI == EPI_LRELU2) {  // buf1 <- leaky_relu(acc, 0.5)^2
           const float t = a > 0.0f ? a : __fmul_rn(a, 0.5f);
           o[i] = __fmul_rn(t, t);
@@ -237,7 +265,7 @@ __device__ __forceinline__ void stage_chunk(const KArgs& p, const uint32_t (&acc
         }
       }
       const uint32_t at = off + (static_cast<uint32_t>(j ^ sw) << 4);
-      if constexpr (epi_act_fwd(EPI) || EPI == EPI_CE_GRAD) {
+      if constexpr (epi_act_fwd(EPI)) {
         st_shared_v4(buf0 + at, pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
                      pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
         st_shared_v4(buf1 + at, pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
@@ -729,13 +757,15 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
           ce_stats_chunk(p, r, col0, ce_row, ce);
           continue;
         }
-        if constexpr (EPI == EPI_CE_GRAD) ce_grad_chunk(p, r, col0, ce_row, ce);
         const uint32_t b = chunk & 1u;
         const uint32_t buf0 = kF32 ? wbuf + b * 4096u : wbuf + b * 2048u;
         const uint32_t buf1 = wbuf + 4096u + b * 2048u;
         if (lane == 0) bulk_wait_read<1>();  // the store that last used buffer b is done reading
         __syncwarp();
-        stage_chunk<EPI>(p, r, rin, buf0, buf1, lane, EPI == EPI_CE_DZ ? ce.scale : 0.0f);
+        if constexpr (EPI == EPI_CE_GRAD)
+          stage_grad_chunk(p, r, col0, ce_row, ce, buf0, buf1, keep_lo, lane);
+        else
+          stage_chunk<EPI>(p, r, rin, buf0, buf1, lane, EPI == EPI_CE_DZ ? ce.scale : 0.0f);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {

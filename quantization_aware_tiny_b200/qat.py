@@ -385,27 +385,19 @@ _FLOAT = {torch.float32: "fp32", torch.bfloat16: "bf16"}
 def _need(where, *specs):
     """Refuses what the C side cannot see from a pointer: specs are (tensor or
     None, dtype, elements at least); every tensor on the current CUDA device."""
-    cur = None
+    cur = torch.cuda.current_device()
     for t, dtype, n in specs:
-        if t is None:
-            continue
-        if not t.is_cuda or t.dtype != dtype or t.numel() < n:
-            raise QatError(QAT_ERR_ARG, where)
-        if cur is None:
-            cur = torch.cuda.current_device()
-        if t.device.index != cur:
+        if t is not None and (t.dtype is not dtype or t.get_device() != cur or t.numel() < n):
             raise QatError(QAT_ERR_ARG, where)
 
 
-def _rows(where, t, cols, T=None, ld=0):
-    """Row stride of a 2-D tensor whose rows hold at least `cols` contiguous elements."""
-    if t.dim() != 2 or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
+def _rows(where, t, cols, T=0):
+    """Row stride of a 2-D tensor of at least T rows that hold at least `cols`
+    contiguous elements."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] < cols or shape[0] < T or (shape[1] > 1 and stride[1] != 1):
         raise QatError(QAT_ERR_ARG, where)
-    if T is not None and t.shape[0] < T:
-        raise QatError(QAT_ERR_ARG, where)
-    if ld == 0:
-        ld = t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0))
-    return ld
+    return stride[0] if shape[0] > 1 else max(cols, stride[0])
 
 
 def _head(where, W, qw):
