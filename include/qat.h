@@ -294,8 +294,7 @@ int qat_rope_freqs(int32_t rotary, double base, int32_t scaling, double factor,
  * they may be column ranges of one Q|K|V projection; lse [heads, Tq] fp32.
  * Sequences: b holds query rows [cu_q[b], cu_q[b+1]) and key rows
  * [cu_k[b], cu_k[b+1]) (device int32 [batch + 1], ascending; offsets are cut to
- * the tensors), none longer than max_q / max_k (longer ones are left
- * unfinished); or, with a NULL table, max_q (max_k) rows each and
+ * the tensors, lengths to max_q / max_k: their first rows are taken); or, with a NULL table, max_q (max_k) rows each and
  * Tq = batch * max_q (Tk = batch * max_k).  Rows of no sequence are left as
  * they are, and nothing that lies in them -- NaN included -- reaches another row.
  * causal != 0: the last query of a sequence is aligned with its last key, query

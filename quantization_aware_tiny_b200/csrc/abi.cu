@@ -811,7 +811,7 @@ int qat_attn_bwd(const qat_attn* a, const qat_bf16* dO, int64_t lddo, const qat_
     return QAT_ERR_SHAPE;
   if (!aligned16(dO) || !aligned16(dQ) || !aligned16(dK) || !aligned16(dV) || !aligned16(workspace))
     return QAT_ERR_ALIGN;
-  if (p.batch == 0) return QAT_OK;
+  if (p.batch == 0 || (p.Tq == 0 && p.Tk == 0)) return QAT_OK;
   Carver ws(workspace, ws_bytes);
   p.delta = static_cast<float*>(ws.take(static_cast<size_t>(p.heads) * p.Tq * 4));
   if (p.Tq > 0 && !p.delta) return QAT_ERR_WORKSPACE;

@@ -4,12 +4,21 @@
 //   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K.
 //
 // Two kernels, each with its sums in tensor memory from first to last:
-//   attn_dq_kernel   a CTA owns 2 x 128 queries of a head and walks the keys
-//   attn_dkv_kernel  a CTA owns 128 keys of a key head and walks the queries of
+//   attn_dq_kernel   a block owns 128 queries of a head and walks the keys
+//   attn_dkv_kernel  a block owns 128 keys of a key head and walks the queries of
 //                    all heads of its group (their gradients meet in the sum)
 // S and dP are thus formed twice, 7 products instead of 5; in return no partial
-// sum ever leaves a CTA: no fp32 copy of dQ in memory, no atomics, and the same
+// sum ever leaves a block: no fp32 copy of dQ in memory, no atomics, and the same
 // inputs give the same bits.
+//
+// Bound by the chain of hand-overs from a block's S to its dS (about 2,500 cycles a
+// 128 x 128 block in dq and 3,300 in dkv at head size 64, where the products take
+// 768 and 1,024 and the exponentials 1,024): tensor memory loads and stores, and
+// barriers, each some 150 to 400 cycles with 16 warps at them.  4 sequences of 4,096
+// tokens, 8 heads of 64 over 4: dq 164 us, dkv 200 us together with it 334 us
+// (515 TFLOP/s of the 5 products that have to be); 8,192 tokens of 128, 8 over 2:
+// 690 us.  Exponentials partly on the multiply-add units, two issuing warps, and P
+// and dS handed over together gained nothing or lost.
 //
 // P and dS are rounded to bf16 for the second products.  They go back to tensor
 // memory and are read from there as operand A.  Both kernels form P as soon as S
@@ -437,7 +446,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
 // P^T, dV, dK.  Issue order: S^T(n + 1) once S^T(n) is read; dV += P^T(n) dO(n)
 // once P(n) is written; dK += dS^T(n) Q(n) and dP^T(n + 1) once dS(n) is.
 // Heads of more than 96 dims leave no columns for P^T: it then replaces S^T, and
-// S^T(n + 1) waits for dV's product (a separate P^T at head size 80: see below).
+// S^T(n + 1) waits for dV's product.
 struct DkvPiece {
   Seq sq;
   int kv_head, key0;       // keys from key0 on
@@ -733,21 +742,17 @@ int launch(const AttnArgs& a, cudaStream_t s) {
   const int64_t qb = (static_cast<int64_t>(a.max_q) + BT - 1) / BT;
   const int64_t kb = (static_cast<int64_t>(a.max_k) + BT - 1) / BT;
   if (qb > 65535 || kb > 65535 || lists > (1ll << 31) - 1) return QAT_ERR_SHAPE;
+  if ((rc = make_head_map(&mq, a.Q, a.hd, a.heads, std::max<int64_t>(a.Tq, 1), a.ldq, BT))) return rc;
+  if ((rc = make_head_map(&mo, a.dO, a.hd, a.heads, std::max<int64_t>(a.Tq, 1), a.lddo, BT))) return rc;
+  if ((rc = make_head_map(&mk, a.K, a.hd, kv_heads, std::max<int64_t>(a.Tk, 1), a.ldk, BT))) return rc;
+  if ((rc = make_head_map(&mv, a.V, a.hd, kv_heads, std::max<int64_t>(a.Tk, 1), a.ldv, BT))) return rc;
   if (a.Tq > 0 && qb > 0) {
-    if ((rc = make_head_map(&mq, a.Q, a.hd, a.heads, a.Tq, a.ldq, BT))) return rc;
-    if ((rc = make_head_map(&mo, a.dO, a.hd, a.heads, a.Tq, a.lddo, BT))) return rc;
-    if ((rc = make_head_map(&mk, a.K, a.hd, kv_heads, std::max<int64_t>(a.Tk, 1), a.ldk, BT))) return rc;
-    if ((rc = make_head_map(&mv, a.V, a.hd, kv_heads, std::max<int64_t>(a.Tk, 1), a.ldv, BT))) return rc;
     attn_dq_kernel<NC><<<dim3(static_cast<unsigned>(lists), static_cast<unsigned>(qb)), C::THREADS,
                          C::SMEM, s>>>(mq, mo, mk, mv, a);
     count_launch();
     if (cudaGetLastError() != cudaSuccess) return QAT_ERR_CUDA;
   }
   if (a.Tk > 0 && kb > 0) {
-    if ((rc = make_head_map(&mq, a.Q, a.hd, a.heads, std::max<int64_t>(a.Tq, 1), a.ldq, BT))) return rc;
-    if ((rc = make_head_map(&mo, a.dO, a.hd, a.heads, std::max<int64_t>(a.Tq, 1), a.lddo, BT))) return rc;
-    if ((rc = make_head_map(&mk, a.K, a.hd, kv_heads, a.Tk, a.ldk, BT))) return rc;
-    if ((rc = make_head_map(&mv, a.V, a.hd, kv_heads, a.Tk, a.ldv, BT))) return rc;
     attn_dkv_kernel<NC><<<dim3(static_cast<unsigned>(lists / a.group), static_cast<unsigned>(kb)), C::THREADS,
                           C::SMEM, s>>>(mq, mo, mk, mv, a);
     count_launch();

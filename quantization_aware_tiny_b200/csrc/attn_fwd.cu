@@ -17,8 +17,13 @@
 // single tokens) leave no second tile.  Both tiles then hold the same queries and
 // take every other key block; their sums are joined at the end.  Where several
 // query heads share a key head, the tile's rows are those of up to 4 heads, so K
-// and V are read once for all of them (256 windows of 64 queries and 1,024 keys,
-// 8 heads of 64 over 4: see below).
+// and V are read once for all of them (256 windows of 64 queries and 1,024 keys, 8
+// heads of 64 over 4: 259 us with a piece per head and one tile, 104 us so).
+//
+// Measured (causal): 8,192 tokens, 8 heads of 128: 128 us, 1,070 TFLOP/s; 16
+// sequences of 1,024, 8 heads of 80: 55 us, 390 TFLOP/s, where a piece has 1 to 8
+// blocks a tile and loading Q, the first scores and writing O show; 64 windows of
+// one token and 4,096 keys, 32 heads of 128 over 8: 203 us, 5.3 TB/s of K and V.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the
 // last time: probabilities then stay below 2^8, which fp32 sums and bf16

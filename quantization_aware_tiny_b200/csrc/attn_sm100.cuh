@@ -204,14 +204,15 @@ struct Seq {
 };
 
 // Sequence b: [cu[b], cu[b+1]) of the packed rows, or rows of equal length.
-// Offsets outside the tensor are cut to it, so no table makes a kernel leave it.
+// Offsets outside the tensor are cut to it, and lengths to max_q / max_k, so no
+// table makes a kernel leave the tensors or read what no block computed.
 __device__ __forceinline__ Seq seq_of(const AttnArgs& p, int b) {
   Seq s;
   if (p.cu_q) {
     const int64_t a = min(max(static_cast<int64_t>(p.cu_q[b]), int64_t{0}), p.Tq);
     const int64_t e = min(max(static_cast<int64_t>(p.cu_q[b + 1]), a), p.Tq);
     s.q0 = a;
-    s.nq = static_cast<int>(e - a);
+    s.nq = min(static_cast<int>(e - a), p.max_q);
   } else {
     s.q0 = static_cast<int64_t>(b) * p.max_q;
     s.nq = p.max_q;
@@ -220,7 +221,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& p, int b) {
     const int64_t a = min(max(static_cast<int64_t>(p.cu_k[b]), int64_t{0}), p.Tk);
     const int64_t e = min(max(static_cast<int64_t>(p.cu_k[b + 1]), a), p.Tk);
     s.k0 = a;
-    s.nk = static_cast<int>(e - a);
+    s.nk = min(static_cast<int>(e - a), p.max_k);
   } else {
     s.k0 = static_cast<int64_t>(b) * p.max_k;
     s.nk = p.max_k;

@@ -134,7 +134,8 @@ int dispatch(const RopeArgs& r, cudaStream_t s) {
   const int half = r.rotary / 2;
   // 16-byte packs where every part of a head starts on a pack's boundary
   // (rows and heads do: head_dim and the row strides are multiples of 8 elements).
-  // Packs against single elements, 65,536 x 12 heads of 64 bf16: see below.
+  // (65,536 tokens of 12 heads of 64 bf16: 37 us, 5.4 TB/s; more packs of a thread in
+  // flight, 2 to 8, gave 38 to 53 us.)
   if (r.interleaved) {
     if (r.rotary % W == 0) return launch<T, W, true>(r, s);
     return launch<T, 2, true>(r, s);

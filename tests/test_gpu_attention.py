@@ -325,6 +325,35 @@ def test_same_bits_every_time_on_two_streams_and_in_a_graph():
         assert all(torch.equal(x, y) for x, y in zip(w, got))
 
 
+def test_tables_that_do_not_fit_are_cut():
+    """Offsets behind the tensors or before them, falling ones, and sequences longer
+    than max_q / max_k: what is left of each is computed, the rest stays as it was."""
+    c = Case([100, 60], tail=0, pad=0, heads=2, kv_heads=1)
+    wide = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    want = Case([100, 60], tail=0, pad=0, heads=2, kv_heads=1)
+    o, lse = want.forward()
+    got, lse2 = c.forward(cu_q=wide([-7, 100, 999]), cu_k=wide([-7, 100, 999]))
+    torch.cuda.synchronize()
+    assert torch.equal(o, got) and torch.equal(lse, lse2)
+    first = Case([64, 0, 60], [64, 0, 60], tail=0, pad=0, heads=2, kv_heads=1)
+    for name in ("Q", "K", "V", "dO"):  # the first 64 rows of 100, and the second sequence
+        src = getattr(c, name)
+        setattr(first, name, torch.cat([src[:64], src[100:]]))
+    fo, flse = first.forward()
+    fg = first.backward(fo, flse)
+    tab = dict(cu_q=wide([0, 100, 100, 160]), cu_k=wide([0, 100, 100, 160]), max_q=64, max_k=64)
+    got, lse2 = c.forward(**tab)
+    grads = c.backward(got, lse2, **tab)
+    torch.cuda.synchronize()
+    keep = torch.cat([torch.arange(64), torch.arange(100, 160)]).cuda()
+    assert torch.equal(got[keep], fo) and bool((got[64:100] == 7).all())
+    for a, b in zip(grads, fg):
+        assert torch.equal(a[keep], b) and bool((a[64:100] == 7).all())
+    falling, _ = c.forward(cu_q=wide([50, 20, 80]), cu_k=wide([50, 20, 80]))
+    torch.cuda.synchronize()
+    assert bool((falling[:20] == 7).all()) and bool((falling[80:] == 7).all()) and qat.device_error() == 0
+
+
 def test_refusals():
     c = Case([64], tail=0, pad=0)
     o, lse = c.forward()

@@ -169,4 +169,5 @@ def test_attention_refusals():
     # nothing to do: no sequences, no rows
     assert attn(batch=0, Tq=0, Tk=0) == qat.QAT_OK and attn(dO=A16, batch=0, Tq=0, Tk=0) == qat.QAT_OK
     assert attn(batch=3, Tq=0, max_q=0, Tk=192) == qat.QAT_OK
+    assert attn(dO=A16, batch=3, Tq=0, max_q=0, Tk=0, max_k=0) == qat.QAT_OK
     assert qat.launch_count() == before
