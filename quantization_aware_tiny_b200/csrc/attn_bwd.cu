@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
           scores(0, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
           scores(0, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
           if (ok) mma_commit(&m.b_empty[base % ST], issue);
+          if (x.steps == 1) mma_commit(m.fix_empty, issue);  // Q and dO: the next piece's may come
           for (int n = 0; ok && n < x.steps; ++n) {
             const int g = base + n;
             const bool more = n + 1 < x.steps;
@@ -305,9 +306,9 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
             if (more) {
               scores(n + 1, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
               if (ok) mma_commit(&m.b_empty[(g + 1) % ST], issue);
+              if (n + 2 == x.steps) mma_commit(m.fix_empty, issue);
             } else {
               mma_commit(m.acc_full, issue);
-              mma_commit(m.fix_empty, issue);
             }
           }
           base += x.steps;
@@ -579,6 +580,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
           ++loads;
           scores(0, at_s, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
           scores(0, at_dp, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
+          if (x.steps == 1) mma_commit(m.fix_empty, issue);  // K and V: the next piece's may come
           for (int n = 0; ok && n < x.steps; ++n) {
             const bool more = n + 1 < x.steps;
             if (apart && more) {
@@ -590,11 +592,9 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
             if (!apart && more) scores(n + 1, at_s, m.a_full, m.ring_a, ring_a, fix_a, 0, m.s_full);
             add(n, m.ds_full, T_DP, C::MC, t_dk, rows_a, m.a_empty);
             if (more) scores(n + 1, at_dp, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
+            if (n + 2 == x.steps) mma_commit(m.fix_empty, issue);
           }
-          if (ok) {
-            mma_commit(m.acc_full, issue);
-            mma_commit(m.fix_empty, issue);
-          }
+          if (ok) mma_commit(m.acc_full, issue);
           base += x.steps;
         }
         if (!ok || !queue.next(pieces, work, lane, m.abort_flag, p.err)) break;
