@@ -380,7 +380,6 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       ok = warp_wait(m.p_full, pieces & 1, m.abort_flag, p.err);
       const float delta = m.rows[quarter * 32 + lane];
       const float2 cc = make_float2(c2, c2), nl = make_float2(-lse2, -lse2), nd = make_float2(-delta, -delta);
-      const uint32_t count = static_cast<uint32_t>(hi - lo);
       for (int n = 0; ok && n < x.steps; ++n) {
         if (!warp_wait(m.s_full, (base + n) & 1, m.abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
@@ -391,12 +390,8 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(m.s_read);
         const int key0 = (x.j0 + n) * BT;
-        if (key0 < full0 || key0 + BT > full1) {
-          const int a = lo - key0 - w * 32;
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (static_cast<uint32_t>(k - a) >= count) s[k] = 0xff800000u;  // -inf
-        }
+        // (a query of a single key has no gradient: dS is 0, where dP and delta differ by roundings)
+        if (key0 < full0 || key0 + BT > full1) mask_scores(s, lo - key0 - w * 32, hi - lo == 1 ? 0 : hi - lo);
         float2 pr[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
@@ -617,7 +612,6 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       const DkvPiece x(p, work);
       int lo, hi;  // queries that see this thread's key
       queries_of(p, x.sq, x.key0 + r, lo, hi);
-      const uint32_t count = static_cast<uint32_t>(hi - lo);
       // lse and delta of the warp's 32 queries, a copy per warp: warps wait for nothing but
       // their barriers; the next block's values are on their way while this one is worked on
       float* buf = m.rows + (warp - 4) * 2 * C::MC;
@@ -635,6 +629,9 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       if (x.steps > 0) fetch();
       int block = 0;  // of the step
       const float2 cc = make_float2(c2, c2);
+      const bool single = x.sq.nk == 1 || p.window == 1;  // every query sees one key at most
+      // under a causal mask the query at key 0's place sees that key alone
+      const int lone = p.causal && x.key0 == 0 ? x.sq.nq - x.sq.nk : -1;
       for (int n = 0; ok && n < x.steps; ++n) {
         const int i0 = (x.j0 + block) * BT;
         if (++block == x.nb) block = 0;
@@ -656,12 +653,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(m.s_read);
         }
-        if (i0 < x.full0 || i0 + BT > x.full1) {
-          const int a = lo - i0 - w * 32;
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (static_cast<uint32_t>(k - a) >= count) s[k] = 0xff800000u;  // -inf
-        }
+        if (i0 < x.full0 || i0 + BT > x.full1) mask_scores(s, lo - i0 - w * 32, hi - lo);
         float2 pr[16];
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
@@ -687,6 +679,13 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
         tc_fence_after();
         tmem_ld32(t + T_DP, s);
         tmem_ld_wait();
+        if (single || (lone >= i0 && lone < i0 + BT)) {
+          // a query of a single key has no gradient: dP is delta (rounded another way)
+          const int at0 = r == 0 ? lone - i0 - w * 32 : -1;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (single || k == at0) s[k] = __float_as_uint(-buf[C::MC + k]);
+        }
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
           const float4 d = *reinterpret_cast<const float4*>(buf + C::MC + 2 * k);

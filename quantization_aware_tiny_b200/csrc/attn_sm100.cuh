@@ -269,6 +269,18 @@ __device__ __forceinline__ void key_blocks(const AttnArgs& p, const Seq& s, int 
   b1 = hi2 > lo2 ? (hi2 + KEYS - 1) / KEYS : b0;
 }
 
+// Scores of 32 neighbouring places of a row, of which [a, a + n) are seen (n = 0:
+// none): the others become -inf.  Rows of a warp lie next to one another, so most
+// such pieces of a masked block are seen by all of them and left alone.
+__device__ __forceinline__ void mask_scores(uint32_t (&s)[32], int a, int n) {
+  const int lo = min(max(a, 0), 32), hi = min(max(a + n, 0), 32);
+  const uint32_t seen = hi > lo ? (0xffffffffu >> (32 - hi + lo)) << lo : 0u;  // bit k: place k
+  if (__any_sync(0xffffffffu, ~seen)) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) s[k] = (seen & (1u << k)) ? s[k] : 0xff800000u;
+  }
+}
+
 // Bytes of a tile of `rows` rows and NC 64-dim chunks; chunk c starts at c * rows * 128.
 __host__ __device__ constexpr int tile_bytes(int rows, int nc) { return rows * 128 * nc; }
 

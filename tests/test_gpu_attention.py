@@ -234,6 +234,29 @@ def test_bwd_flat_and_peaked_rows(peak):
     Case([700], heads=1, kv_heads=1, peak=peak).check_backward()
 
 
+@pytest.mark.parametrize("kw", [dict(lq=[70, 3], window=1), dict(lq=[5, 300], lk=[1, 1], causal=False),
+                                dict(lq=[5, 300], lk=[1, 1]), dict(lq=[1, 1, 1])])
+def test_bwd_single_key_has_no_gradient(kw):
+    """A softmax over one key is constant: dQ and dK are exactly zero."""
+    c = Case(heads=2, kv_heads=1, hd=80, **kw)
+    c.check_backward()
+    o, lse = c.forward()
+    dq, dk, dv = c.backward(o, lse)
+    torch.cuda.synchronize()
+    assert not dq[:c.nq, :160].any() and not dk[:c.nk, :80].any() and dv[:c.nk, :80].any()
+
+
+def test_bwd_first_row_of_a_causal_sequence():
+    """The row that sees key 0 only: its dQ is exactly zero, the next one's is not."""
+    for lq, lk in (([200], [200]), ([300], [170])):
+        c = Case(lq, lk, heads=2, kv_heads=2)
+        o, lse = c.forward()
+        dq = c.backward(o, lse)[0]
+        torch.cuda.synchronize()
+        first = lq[0] - lk[0]
+        assert not dq[:first + 1, :128].any() and dq[first + 1, :128].any()
+
+
 def test_bwd_scale():
     Case([150], scale=0.7).check_backward()
 
