@@ -128,7 +128,64 @@ def core_train(T):
         core.backward(dY)
 
 
-CASES = {"core_train": core_train, "logits_fwd": logits_fwd, "logits_fwd_fused": logits_fwd_fused, "head_dw": head_dw, "head_dx": head_dx,
+def _attention(T, head_dim, seq_len):
+    """One attention call's tensors: T tokens in sequences of seq_len, 8 query
+    heads over 4, queries, keys and values as columns of one projection."""
+    H, KH, bf = 8, 4, torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(0)
+    qkv = torch.randn(T, (H + 2 * KH) * head_dim, device="cuda", generator=g).to(bf)
+    q, k, v = (qkv[:, :H * head_dim], qkv[:, H * head_dim:(H + KH) * head_dim],
+               qkv[:, (H + KH) * head_dim:])
+    o, lse = torch.empty(T, H * head_dim, dtype=bf, device="cuda"), torch.empty(H, T, device="cuda")
+    fwd = lambda: qat.qat_attn_fwd(q, k, v, o, lse, H, KH, head_dim, max_q=seq_len)
+    fwd()
+    return q, k, v, o, lse, fwd
+
+
+def attn_fwd(T):
+    """Causal attention of the 640-wide core: sequences of 1,024 tokens, heads of 80."""
+    fwd = _attention(T, 80, 1024)[-1]
+    for _ in range(3):
+        fwd()
+
+
+def attn_bwd(T):
+    """Its backward (two kernels: dQ, and dK with dV)."""
+    q, k, v, o, lse, _ = _attention(T, 80, 1024)
+    dO = torch.randn_like(o)
+    grads = [torch.empty(t.shape, dtype=t.dtype, device="cuda") for t in (q, k, v)]
+    ws = torch.empty(qat.workspace_size(qat.QAT_OP_ATTN_BWD, 8, 80, T, False), dtype=torch.uint8,
+                     device="cuda")
+    for _ in range(3):
+        qat.qat_attn_bwd(dO, q, k, v, o, lse, *grads, 8, 4, 80, max_q=1024, workspace=ws)
+
+
+def cross_entropy(T):
+    """The tied 8,192-word head's loss and gradients."""
+    c = sy.head_mlp_case(T=1, seed=0)
+    q = qat.quantize_weight(torch.from_numpy(c["Wemb"]).cuda(), 8)
+    Z = sy.act_bf16(np.random.default_rng(1), T, 512).cuda()
+    t = torch.randint(0, 8192, (T,), device="cuda")
+    loss, lse, mean = (torch.empty(n, device="cuda") for n in (T, T, 2))
+    dZ, dW = torch.empty_like(Z), torch.empty(8192, 512, device="cuda")
+    ws = torch.empty(qat.workspace_size(qat.QAT_OP_CE_BWD, 8192, 512, T, False), dtype=torch.uint8,
+                     device="cuda")
+    for _ in range(3):
+        qat.qat_ce_fwd(Z, t, loss, lse, 8, qw=q, mean=mean, workspace=ws)
+        qat.qat_ce_bwd(Z, t, lse, 8, qw=q, gscale=mean[1:], dZ=dZ, dW=dW, workspace=ws)
+
+
+def rope(T):
+    """Rotary positions of queries and keys (12 heads of 64 in rows of 1,024)."""
+    x = torch.randn(T, 1024, device="cuda").to(torch.bfloat16)
+    y = torch.empty(T, 768, dtype=torch.bfloat16, device="cuda")
+    f = qat.rope_freqs(64)[0]
+    for _ in range(3):
+        qat.qat_rope(x[:, :768], y, 12, 64, f, seq_len=1024)
+
+
+CASES = {"attn_fwd": attn_fwd, "attn_bwd": attn_bwd, "cross_entropy": cross_entropy, "rope": rope,
+         "core_train": core_train, "logits_fwd": logits_fwd, "logits_fwd_fused": logits_fwd_fused, "head_dw": head_dw, "head_dx": head_dx,
          "mlp_step": mlp_step, "export_state_dict": export_state_dict, "dequant_state_dict": dequant_state_dict,
          "quantize_step_weights": quantize_step_weights}
 
