@@ -218,8 +218,9 @@ int qat_mlp_bwd(const float* Wfc, const float* Wproj, const qat_qweight* qfc,
  * -100, say) counts for nothing -- loss 0, gradient 0; its lse is written.
  * loss, lse [T] fp32.  mean (nullable, 2 floats): the mean loss over the
  * counted tokens and 1 / their number (0 and 0 when there are none).
- * Statistics are fp32, the mean's sum fp64; the results do not depend on
- * timing.  workspace: qat_workspace_size(QAT_OP_CE_FWD, V, d, T, raw) bytes.
+ * Z holds finite values in every row (a NaN of a row without target would reach
+ * dW: its zero gradient is multiplied with the row).  Statistics are fp32, the
+ * mean's sum fp64; the same inputs give the same bits.  workspace: qat_workspace_size(QAT_OP_CE_FWD, V, d, T, raw) bytes.
  * T = 0 writes mean only.
  * ------------------------------------------------------------------------- */
 int qat_ce_fwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int32_t bits,
@@ -236,7 +237,9 @@ int qat_ce_fwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
  * target get zero rows of dZ.  The logits are computed again and turned into g
  * a piece of tokens at a time: g exists only for one piece, as bf16 plus the
  * bf16 of what that rounding left (dZ takes the first, and the second at
- * the target; dW takes both, so it is good to about 1e-5).  workspace: qat_workspace_size(QAT_OP_CE_BWD, V, d, T, raw)
+ * the target; dW takes both, so it is good to about 1e-5).  dZ has the same bits
+ * every time; dW's partial sums are added in order where V * d fills the GPU with
+ * output tiles, else as they come, as in qat_linear_bwd.  workspace: qat_workspace_size(QAT_OP_CE_BWD, V, d, T, raw)
  * bytes give the pieces that run fastest and also serve qat_ce_fwd; less works
  * with smaller pieces, down to 256 tokens (1024 bytes per word, V rounded up
  * to a multiple of 8, and 1 KiB beside the operand), below which QAT_ERR_WORKSPACE is

@@ -1,9 +1,9 @@
 // Attention forward on tcgen05: O = softmax(scale Q K^T + mask) V in one pass
 // over the keys with a running maximum and sum.
 //
-// A piece of work is two tiles of 128 queries of one head, walked over the keys in
-// blocks of 128, so that every staged K and V block serves 256 queries and the
-// tensor core works on one tile while the other's softmax runs:
+// A piece of work is two tiles of 128 queries, of two heads of a group or of one
+// head, walked over the keys in blocks of 128, so that every staged K and V block
+// serves both and the tensor core works on one tile while the other's softmax runs:
 //   warp 0      TMA producer: Q, then K and V blocks through a ring
 //   warp 1      MMA issuer: S = Q K^T, then O += P V with P read as operand A
 //               straight from tensor memory
@@ -21,7 +21,7 @@
 // heads of 64 over 4: 259 us with a piece per head and one tile, 104 us so).
 //
 // Measured (causal): 8,192 tokens, 8 heads of 128: 128 us, 1,070 TFLOP/s; 16
-// sequences of 1,024, 8 heads of 80: 55 us, 390 TFLOP/s, where a piece has 1 to 8
+// sequences of 1,024, 8 heads of 80: 52 us, 415 TFLOP/s, where a piece has 1 to 8
 // blocks a tile and loading Q, the first scores and writing O show; 64 windows of
 // one token and 4,096 keys, 32 heads of 128 over 8: 203 us, 5.3 TB/s of K and V.
 //
@@ -55,9 +55,15 @@ struct Cfg {
   static constexpr float RESCALE = 8.0f;
 };
 
+// What the two tiles of a piece hold: 256 queries of one head, 128 queries of two
+// heads of a group (both tiles then see the same key blocks), or short queries.
+enum Mode : int { kRows, kHeads, kShort };
+
 // A piece of work: which rows, which keys.
-template <bool SHORT>
+template <int MODE>
 struct Piece {
+  static constexpr bool SHORT = MODE == kShort;
+  static constexpr bool HEADS = MODE == kHeads;
   Seq sq;
   int head, kv_head;  // first (or only) head
   int heads;          // SHORT: heads in the tile
@@ -67,6 +73,7 @@ struct Piece {
   bool live;
 
   __device__ Piece(const AttnArgs& p, const Work& w) {
+    static_assert(!(SHORT && HEADS), "one mode");
     if constexpr (SHORT) {
       const int per = BQ / p.rows, chunks = (p.group + per - 1) / per;
       const int kv_heads = p.heads / p.group;
@@ -82,15 +89,16 @@ struct Piece {
       b0[1] = j0 + 1;
       b1[0] = b1[1] = j1;
     } else {
-      head = w.list % p.heads;
+      const int lists = HEADS ? p.heads / 2 : p.heads;
+      head = w.list % lists * (HEADS ? 2 : 1);
       kv_head = head / p.group;
       heads = 1;
-      sq = seq_of(p, w.list / p.heads);
+      sq = seq_of(p, w.list / lists);
       // late query blocks see most keys under a causal mask: they come first
-      i0 = (static_cast<int>(gridDim.y) - 1 - w.block) * 2 * BQ;
+      i0 = (static_cast<int>(gridDim.y) - 1 - w.block) * (HEADS ? BQ : 2 * BQ);
       live = i0 < sq.nq;
       key_blocks<BQ, BKV>(p, sq, i0, b0[0], b1[0]);
-      key_blocks<BQ, BKV>(p, sq, i0 + BQ, b0[1], b1[1]);
+      key_blocks<BQ, BKV>(p, sq, HEADS ? i0 : i0 + BQ, b0[1], b1[1]);
       j0 = b1[0] > b0[0] ? b0[0] : b0[1];
       if (b1[1] > b0[1]) j0 = min(j0, b0[1]);
       j1 = max(max(b1[0], b1[1]), j0);
@@ -107,11 +115,12 @@ struct Piece {
   __device__ bool last(int w, int j) const { return j + STEP >= to(w); }
 };
 
-template <int NC, bool SHORT>
+template <int NC, int MODE>
 __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const AttnArgs p) {
   using C = Cfg<NC>;
+  constexpr bool SHORT = MODE == kShort, HEADS = MODE == kHeads;
   constexpr int ST = C::ST;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -186,7 +195,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       bool ok = true;
       for (bool more = true; more; ++pieces) {
         if (lane == 0) {
-          const Piece<SHORT> x(p, work);
+          const Piece<MODE> x(p, work);
           if (x.j1 > x.j0) {
             ok = loads == 0 || mbar_wait(q_empty, (loads - 1) & 1, abort_flag, p.err);
             if (ok) {
@@ -197,11 +206,12 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
                   for (int c = 0; c < NC; ++c)
                     tma_load_3d(&tmQ, q_full, sQ + c * BQ * 128 + h * p.rows * 128, c * 64, x.head + h, row);
               } else {
-                const int tiles = x.i0 + BQ < x.sq.nq ? 2 : 1;
+                const int tiles = HEADS || x.i0 + BQ < x.sq.nq ? 2 : 1;
                 mbar_arrive_expect_tx(q_full, tiles * C::TILE);
                 for (int w = 0; w < tiles; ++w)
                   for (int c = 0; c < NC; ++c)
-                    tma_load_3d(&tmQ, q_full, sQ + w * C::TILE + c * BQ * 128, c * 64, x.head, row + w * BQ);
+                    tma_load_3d(&tmQ, q_full, sQ + w * C::TILE + c * BQ * 128, c * 64, x.head + (HEADS ? w : 0),
+                                row + (HEADS ? 0 : w * BQ));
               }
               ++loads;
             }
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       int n = 0, loads = 0;  // K, V blocks; Q tiles
       bool ok = true;
       for (int pieces = 0;; ++pieces) {
-        const Piece<SHORT> x(p, work);
+        const Piece<MODE> x(p, work);
         if (x.j1 > x.j0) {
           ok = warp_wait(q_full, loads & 1, abort_flag, p.err);
           ++loads;
@@ -309,10 +319,10 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     uint32_t ph = 0, oph = 0, oph1 = 0, mph = 0;  // oph: the own tile's O, oph1: SHORT, tile 1's
     bool ok = true;
     for (int pieces = 0;; ++pieces) {
-      const Piece<SHORT> x(p, work);
+      const Piece<MODE> x(p, work);
       // this warp's 32 rows are queries i0 + r0 .. of one head; the tile's rows start at query `first`
-      const int first = SHORT ? 0 : x.i0 + w * BQ;
-      const int h = SHORT ? quarter * 32 / p.rows : 0;
+      const int first = SHORT ? 0 : HEADS ? x.i0 : x.i0 + w * BQ;
+      const int h = SHORT ? quarter * 32 / p.rows : HEADS ? w : 0;
       const int r0 = SHORT ? quarter * 32 % p.rows : first + quarter * 32;
       const int i = r0 + lane;
       int lo, hi;
@@ -470,26 +480,28 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
   }
 }
 
-template <int NC, bool SHORT>
+template <int NC, int MODE>
 int launch(const AttnArgs& a, cudaStream_t s) {
   using C = Cfg<NC>;
+  constexpr bool SHORT = MODE == kShort, HEADS = MODE == kHeads;
   static std::atomic<uint64_t> done{0};
-  int rc = allow_smem(reinterpret_cast<const void*>(attn_fwd_kernel<NC, SHORT>), C::SMEM, done);
+  int rc = allow_smem(reinterpret_cast<const void*>(attn_fwd_kernel<NC, MODE>), C::SMEM, done);
   if (rc) return rc;
   CUtensorMap mq, mk, mv;
   const int kv_heads = a.heads / a.group;
   if ((rc = make_head_map(&mq, a.Q, a.hd, a.heads, a.Tq, a.ldq, SHORT ? a.rows : BQ))) return rc;
   if ((rc = make_head_map(&mk, a.K, a.hd, kv_heads, std::max<int64_t>(a.Tk, 1), a.ldk, BKV))) return rc;
   if ((rc = make_head_map(&mv, a.V, a.hd, kv_heads, std::max<int64_t>(a.Tk, 1), a.ldv, BKV))) return rc;
-  int64_t blocks = (static_cast<int64_t>(a.max_q) + 2 * BQ - 1) / (2 * BQ);
-  int64_t lists = static_cast<int64_t>(a.heads) * a.batch;
+  constexpr int rows = HEADS ? BQ : 2 * BQ;  // queries of a piece
+  int64_t blocks = (static_cast<int64_t>(a.max_q) + rows - 1) / rows;
+  int64_t lists = static_cast<int64_t>(HEADS ? a.heads / 2 : a.heads) * a.batch;
   if (SHORT) {
     const int per = BQ / a.rows;
     blocks = 1;
     lists = static_cast<int64_t>(kv_heads) * ((a.group + per - 1) / per) * a.batch;
   }
   if (blocks > 65535 || lists > (1ll << 31) - 1) return QAT_ERR_SHAPE;
-  attn_fwd_kernel<NC, SHORT><<<dim3(static_cast<unsigned>(lists), static_cast<unsigned>(blocks)), C::THREADS,
+  attn_fwd_kernel<NC, MODE><<<dim3(static_cast<unsigned>(lists), static_cast<unsigned>(blocks)), C::THREADS,
                                C::SMEM, s>>>(mq, mk, mv, a);
   count_launch();
   return cuda_status(cudaGetLastError());
@@ -499,11 +511,19 @@ int launch(const AttnArgs& a, cudaStream_t s) {
 
 int launch_attn_fwd(AttnArgs a, cudaStream_t stream) {
   a.err = device_error_ptr();
-  if (a.max_q > BQ) return a.hd <= 64 ? launch<1, false>(a, stream) : launch<2, false>(a, stream);
+  if (a.max_q > BQ) {
+    // Two heads of a group where it has an even number: both tiles then walk the same
+    // blocks.  Against 256 rows of one head (of which the later 128 see one block more):
+    // 16 x 1,024 tokens, 8 heads of 64 / 80 / 128: 52.1 -> 47.2, 55.2 -> 51.8, 58.3 ->
+    // 55.7 us; 8,192 tokens of 128: 127.9 -> 127.5 us.
+    if (a.group % 2 == 0)
+      return a.hd <= 64 ? launch<1, kHeads>(a, stream) : launch<2, kHeads>(a, stream);
+    return a.hd <= 64 ? launch<1, kRows>(a, stream) : launch<2, kRows>(a, stream);
+  }
   // rows per head: as few as hold the queries, but no fewer than the group's heads can fill
   a.rows = BQ;
   while (a.rows > 32 && a.rows / 2 >= a.max_q && BQ / a.rows < a.group) a.rows /= 2;
-  return a.hd <= 64 ? launch<1, true>(a, stream) : launch<2, true>(a, stream);
+  return a.hd <= 64 ? launch<1, kShort>(a, stream) : launch<2, kShort>(a, stream);
 }
 
 }  // namespace qat

@@ -400,6 +400,13 @@ def _rows(where, t, cols, T=0):
     return stride[0] if shape[0] > 1 else max(cols, stride[0])
 
 
+def _whole(where, *tensors):
+    """Refuses tensors with gaps (the C side takes an address and a count)."""
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            raise QatError(QAT_ERR_ARG, where)
+
+
 def _head(where, W, qw):
     if (W is None) == (qw is None):
         raise QatError(QAT_ERR_ARG, where)
@@ -422,6 +429,7 @@ def qat_ce_fwd(Z, targets, loss, lse, bits, W=None, qw=None, mean=None, workspac
     ldz = _rows(f, Z, d)
     _need(f, (Z, torch.bfloat16, 0), (targets, torch.int64, T), (loss, f32, T), (lse, f32, T),
           (mean, f32, 2))
+    _whole(f, targets, loss, lse, mean)
     ws, wsb = _ws(workspace)
     _check(lib().qat_ce_fwd(_p(W), _qref(qw), V, d, bits, _p(Z), ldz, T, _p(targets), _p(loss),
                             _p(lse), _p(mean), ws, wsb, _stream(stream)), f)
@@ -437,9 +445,7 @@ def qat_ce_bwd(Z, targets, lse, bits, W=None, qw=None, dloss=None, gscale=None, 
     ldz = _rows(f, Z, d)
     _need(f, (Z, torch.bfloat16, 0), (targets, torch.int64, T), (lse, f32, T), (dloss, f32, T),
           (gscale, f32, 1), (dZ, torch.bfloat16, T * d), (dW, f32, V * d))
-    for t in (targets, lse, dloss, dZ, dW):
-        if t is not None and not t.is_contiguous():
-            raise QatError(QAT_ERR_ARG, f)
+    _whole(f, targets, lse, dloss, dZ, dW)
     ws, wsb = _ws(workspace)
     _check(lib().qat_ce_bwd(_p(W), _qref(qw), V, d, bits, _p(Z), ldz, T, _p(targets), _p(lse),
                             _p(dloss), _p(gscale), _p(dZ), _p(dW), int(bool(accumulate_dW)), ws,
@@ -471,9 +477,7 @@ def qat_rope(X, Y, heads, head_dim, freqs, positions=None, seq_len=0, interleave
         raise QatError(QAT_ERR_ARG, f)
     ldx, ldy = _rows(f, X, width), _rows(f, Y, width, T)
     _need(f, (X, X.dtype, 0), (Y, X.dtype, 0), (freqs, torch.float64, 1), (positions, torch.int64, T))
-    for t in (freqs, positions):
-        if t is not None and not t.is_contiguous():
-            raise QatError(QAT_ERR_ARG, f)
+    _whole(f, freqs, positions)
     dt = QAT_DTYPE_BF16 if X.dtype == torch.bfloat16 else QAT_DTYPE_F32
     _check(lib().qat_rope(_p(X), ldx, _p(Y), ldy, dt, T, heads, head_dim, 2 * freqs.numel(),
                           _p(freqs), float(scale), _p(positions), int(seq_len),
@@ -490,9 +494,7 @@ def _attn(where, Q, K, V, O, lse, heads, kv_heads, head_dim, causal, window, sca
         cu_k, max_k = cu_q, max_q
     _need(where, (Q, bf, 0), (K, bf, 0), (V, bf, 0), (O, bf, 0), (lse, torch.float32, heads * Tq),
           (cu_q, torch.int32, 1), (cu_k, torch.int32, 1))
-    for t in (lse, cu_q, cu_k):
-        if t is not None and not t.is_contiguous():
-            raise QatError(QAT_ERR_ARG, where)
+    _whole(where, lse, cu_q, cu_k)
     if cu_q is not None:
         batch = cu_q.numel() - 1
     elif cu_k is not None:

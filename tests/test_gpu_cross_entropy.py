@@ -233,6 +233,7 @@ def test_ce_refusals():
     bad(qat.QAT_ERR_ARG, c["Zd"], c["td"][:4], loss, lse, 8, **ok)
     bad(qat.QAT_ERR_ARG, c["Zd"], c["t"], loss, lse, 8, **ok)
     bad(qat.QAT_ERR_ARG, c["Zd"], c["td"], loss, lse, 7, **ok)
+    bad(qat.QAT_ERR_ARG, c["Zd"], c["td"], torch.empty(2 * T, device="cuda")[::2], lse, 8, **ok)
     bad(qat.QAT_ERR_ARG, c["Zd"], c["td"], loss, lse, 8, workspace=ws)
     bad(qat.QAT_ERR_ARG, c["Zd"][:, :32], c["td"], loss, lse, 8, **ok)
     bad(qat.QAT_ERR_ARG, c["Zd"].t().contiguous().t(), c["td"], loss, lse, 8, **ok)
