@@ -119,6 +119,13 @@ def test_fwd_lengths(n, mask):
 
 
 @pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("n", [129, 256, 257, 383, 600])
+def test_fwd_lengths_of_heads_that_share_nothing(n, mask):
+    """As many key heads as query heads: both tiles are of one head."""
+    Case([n, 40], heads=2, kv_heads=2, **mask).check_forward()
+
+
+@pytest.mark.parametrize("mask", MASKS)
 @pytest.mark.parametrize("lens", [([64, 64], [300, 129]), ([300, 1, 5], [64, 1, 0]), ([130], [129]),
                                   ([1, 1, 1], [1, 200, 513]), ([0, 257, 0], [3, 257, 0])])
 def test_fwd_queries_and_keys_of_other_lengths(lens, mask):
