@@ -393,11 +393,16 @@ def _need(where, *specs):
 
 def _rows(where, t, cols, T=0):
     """Row stride of a 2-D tensor of at least T rows that hold at least `cols`
-    contiguous elements."""
+    contiguous elements.  Rows that share memory (a broadcast one: stride 0, which
+    the C side would take for contiguous rows) are refused."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[1] < cols or shape[0] < T or (shape[1] > 1 and stride[1] != 1):
         raise QatError(QAT_ERR_ARG, where)
-    return stride[0] if shape[0] > 1 else max(cols, stride[0])
+    if shape[0] <= 1:
+        return cols
+    if stride[0] < cols:
+        raise QatError(QAT_ERR_ARG, where)
+    return stride[0]
 
 
 def _whole(where, *tensors):

@@ -171,3 +171,20 @@ def test_attention_refusals():
     assert attn(batch=3, Tq=0, max_q=0, Tk=192) == qat.QAT_OK
     assert attn(dO=A16, batch=3, Tq=0, max_q=0, Tk=0, max_k=0) == qat.QAT_OK
     assert qat.launch_count() == before
+
+
+# ------------------------------------------------------------------ binding
+
+def test_rows_that_share_memory_are_refused():
+    """A broadcast row (the gradient of a sum) has stride 0, which the C side takes for
+    contiguous rows: it would read memory behind the tensor."""
+    row = torch.zeros(1, 64)
+    for t in (row.expand(8, 64), torch.zeros(100).as_strided((3, 64), (8, 1))):
+        with pytest.raises(qat.QatError) as e:
+            qat._rows("call", t, 64)
+        assert e.value.code == qat.QAT_ERR_ARG
+    wide = torch.zeros(8, 200)
+    assert qat._rows("call", wide[:, 8:72], 64) == 200
+    # the stride of a single row, or of none, says nothing
+    assert qat._rows("call", row.expand(1, 64), 64) == qat._rows("call", torch.zeros(1, 203)[:, :64], 64) == 64
+    assert qat._rows("call", wide[:0, :64], 64) == 64
