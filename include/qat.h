@@ -243,7 +243,7 @@ int qat_ce_fwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
  * bytes give the pieces that run fastest and also serve qat_ce_fwd; less works
  * with smaller pieces, down to 256 tokens (1024 bytes per word, V rounded up
  * to a multiple of 8, and 1 KiB beside the operand), below which QAT_ERR_WORKSPACE is
- * returned.  With T = 0, dW is zeroed unless accumulate_dW. */
+ * returned.  dZ and dW must not overlap Z.  With T = 0, dW is zeroed unless accumulate_dW. */
 int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int32_t bits,
                const qat_bf16* Z, int64_t ldz, int64_t T, const int64_t* targets, const float* lse,
                const float* dloss, const float* gscale, qat_bf16* dZ, float* dW,
@@ -305,7 +305,9 @@ int qat_rope_freqs(int32_t rotary, double base, int32_t scaling, double factor,
  * last `window` of these.  A query that sees no key gets O = 0, lse = -inf and
  * no gradient.  scale > 0, or 0 for 1 / sqrt(head_dim).  head_dim a multiple of
  * 8 up to 128.  Products and sums are fp32; P and dS are rounded to bf16 as
- * operands of the second products.  The same inputs give the same bits.
+ * operands of the second products.  The same inputs give the same bits.  Outputs
+ * share no elements with inputs or with one another (interleaved columns of one
+ * wider row are fine).  max_q, and for the backward max_k, up to 65,535 * 128.
  * ------------------------------------------------------------------------- */
 #define QAT_ATTN_MAX_HEAD_DIM 128
 typedef struct qat_attn {

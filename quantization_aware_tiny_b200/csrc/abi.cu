@@ -661,6 +661,7 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
   void* glo = ws.take(static_cast<size_t>(rows) * ldg * 2);
   float* rem = static_cast<float*>(ws.take(static_cast<size_t>(rows) * 4));
   if (!ghi || !glo || !rem) return QAT_ERR_WORKSPACE;
+  if (dZ == Z) return QAT_ERR_ARG;  // dW reads the rows of Z after their dZ is written
   for (int64_t t0 = 0; t0 < T; t0 += rows) {
     const int64_t n = std::min(rows, T - t0);
     const qat_bf16* Zp = Z + t0 * ldz;
@@ -790,6 +791,7 @@ int qat_attn_fwd(const qat_attn* a, const qat_bf16* Q, const qat_bf16* K, const 
   const int rc = attn_args(a, Q, K, V, O, lse, &p);
   if (rc) return rc;
   if (p.Tq == 0 || p.batch == 0 || p.max_q == 0) return QAT_OK;
+  if (O == Q || O == K || O == V) return QAT_ERR_ARG;
   return launch_attn_fwd(p, stream);
 }
 
@@ -815,6 +817,11 @@ int qat_attn_bwd(const qat_attn* a, const qat_bf16* dO, int64_t lddo, const qat_
   Carver ws(workspace, ws_bytes);
   p.delta = static_cast<float*>(ws.take(static_cast<size_t>(p.heads) * p.Tq * 4));
   if (p.Tq > 0 && !p.delta) return QAT_ERR_WORKSPACE;
+  // the second kernel reads Q, K, V and dO when dQ is written already
+  for (const qat_bf16* g : {dQ, dK, dV})
+    for (const qat_bf16* in : {Q, K, V, O, dO})
+      if (g && g == in) return QAT_ERR_ARG;
+  if ((dQ && (dQ == dK || dQ == dV)) || (dK && dK == dV)) return QAT_ERR_ARG;
   p.dO = dO;
   p.dQ = dQ;
   p.dK = dK;

@@ -173,6 +173,23 @@ def test_attention_refusals():
     assert qat.launch_count() == before
 
 
+# --------------------------------------------------- outputs in inputs' places
+
+def test_outputs_in_the_place_of_inputs_are_refused():
+    P = [ctypes.c_void_p(0x100000 * i) for i in range(1, 10)]
+    Q, K, V, O, dO, dQ, dK, dV, lse = P
+    before = qat.launch_count()
+    for at in (Q, K, V):
+        assert attn(Q=Q, K=K, V=V, O=at, lse=lse) == qat.QAT_ERR_ARG
+    base = dict(Q=Q, K=K, V=V, O=O, lse=lse, dO=dO, dQ=dQ, dK=dK, dV=dV)
+    for name in ("dQ", "dK", "dV"):
+        for at in (Q, K, V, O, dO) + tuple(base[n] for n in ("dQ", "dK", "dV") if n != name):
+            assert attn(**{**base, name: at}) == qat.QAT_ERR_ARG, name
+    for dW in (None, O):
+        assert ce_bwd(qw=operand(64, 64), Z=Q, dZ=Q, dW=dW) == qat.QAT_ERR_ARG
+    assert qat.launch_count() == before
+
+
 # ------------------------------------------------------------------ binding
 
 def test_rows_that_share_memory_are_refused():
