@@ -495,8 +495,12 @@ def _attn(where, Q, K, V, O, lse, heads, kv_heads, head_dim, causal, window, sca
     queries do; without a table the rows are sequences of max_q (max_k) each."""
     bf, wq, wk = torch.bfloat16, heads * head_dim, kv_heads * head_dim
     Tq, Tk = Q.shape[0], K.shape[0]
-    if cu_k is None and max_k == 0:
+    if cu_k is None and not max_k:
         cu_k, max_k = cu_q, max_q
+    # the C side takes 32 bits, scale 0 for its default, and cuts lengths to max_q and max_k
+    if (max_q is None or max_k is None or (scale is not None and not 2.0 ** -126 <= scale < 2.0 ** 127)
+            or (heads | kv_heads | head_dim | window | max_q | max_k) >> 31):
+        raise QatError(QAT_ERR_ARG, where)
     _need(where, (Q, bf, 0), (K, bf, 0), (V, bf, 0), (O, bf, 0), (lse, torch.float32, heads * Tq),
           (cu_q, torch.int32, 1), (cu_k, torch.int32, 1))
     _whole(where, lse, cu_q, cu_k)
@@ -516,11 +520,12 @@ def _attn(where, Q, K, V, O, lse, heads, kv_heads, head_dim, causal, window, sca
 
 
 def qat_attn_fwd(Q, K, V, O, lse, heads, kv_heads, head_dim, causal=True, window=0, scale=None,
-                 cu_q=None, cu_k=None, max_q=0, max_k=0, stream=None):
+                 cu_q=None, cu_k=None, max_q=None, max_k=None, stream=None):
     """O = softmax(scale Q K^T) V and lse [heads, Tq] fp32, grouped queries.  Rows
     [T, heads * head_dim] bf16 of any stride; sequences by cu_q / cu_k (int32
-    offsets [batch + 1], none longer than max_q / max_k), or max_q (max_k) rows
-    each.  Without cu_k and max_k the keys lie as the queries do."""
+    offsets [batch + 1], none longer than max_q / max_k, which a table needs), or
+    max_q (max_k) rows each.  Without cu_k and max_k the keys lie as the queries do.
+    scale: None for 1 / sqrt(head_dim)."""
     f = "qat_attn_fwd"
     a = _attn(f, Q, K, V, O, lse, heads, kv_heads, head_dim, causal, window, scale, cu_q, cu_k,
               max_q, max_k)
@@ -529,7 +534,7 @@ def qat_attn_fwd(Q, K, V, O, lse, heads, kv_heads, head_dim, causal=True, window
 
 
 def qat_attn_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, heads, kv_heads, head_dim, causal=True, window=0,
-                 scale=None, cu_q=None, cu_k=None, max_q=0, max_k=0, workspace=None, stream=None):
+                 scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None, workspace=None, stream=None):
     """dQ, dK, dV of qat_attn_fwd from dO and what the forward read and wrote
     (the other arguments as there).  All bf16, rows of any stride."""
     f, bf, wq, wk = "qat_attn_bwd", torch.bfloat16, heads * head_dim, kv_heads * head_dim

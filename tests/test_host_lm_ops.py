@@ -205,3 +205,26 @@ def test_rows_that_share_memory_are_refused():
     # the stride of a single row, or of none, says nothing
     assert qat._rows("call", row.expand(1, 64), 64) == qat._rows("call", torch.zeros(1, 203)[:, :64], 64) == 64
     assert qat._rows("call", wide[:0, :64], 64) == 64
+
+
+def test_attention_arguments_that_32_bits_do_not_hold(monkeypatch):
+    """What the C side would wrap to another value, take for its default, or cut every
+    sequence to: refused before a tensor is looked at."""
+    monkeypatch.setattr(qat, "_need", lambda *a: None)
+    rows = lambda w: torch.zeros(64, w, dtype=torch.bfloat16)
+    q, k, lse = rows(128), rows(64), torch.zeros(2, 64)
+    cu = torch.tensor([0, 64], dtype=torch.int32)
+
+    def descriptor(heads=2, kv=1, hd=64, window=0, scale=None, cu_q=cu, cu_k=None, max_q=64, max_k=None):
+        return qat._attn("call", q, k, k, q, lse, heads, kv, hd, True, window, scale, cu_q, cu_k, max_q, max_k)
+
+    a = descriptor(window=(1 << 31) - 1, scale=2.0 ** -126)
+    assert (a.batch, a.max_q, a.max_k, a.window, a.scale) == (1, 64, 64, (1 << 31) - 1, 2.0 ** -126)
+    a = descriptor(cu_q=None)
+    assert (a.batch, a.max_k, a.cu_k, a.scale) == (1, 64, None, 0.0)
+    for kw in (dict(window=1 << 32), dict(window=-1), dict(scale=0.0), dict(scale=1e-46), dict(scale=-1.0),
+               dict(scale=float("nan")), dict(scale=float("inf")), dict(max_q=None), dict(max_q=1 << 32),
+               dict(cu_k=cu), dict(cu_q=None, max_q=None), dict(cu_q=None, max_q=None, max_k=64)):
+        with pytest.raises(qat.QatError) as e:
+            descriptor(**kw)
+        assert e.value.code == qat.QAT_ERR_ARG, kw
