@@ -11,7 +11,8 @@ class CoreAttention:
     """The attention of a core's block: `heads` query heads over `kv_heads` key
     and value heads, causal (optionally the last `window` keys only), on
     sequences of seq_len rows each, or packed ones given by cu (int32 row
-    offsets [batch + 1] on the device, none longer than seq_len).  rope, when
+    offsets [batch + 1] on the device, none longer than seq_len); rows of no
+    sequence attend to nothing (their output and gradient are zero).  rope, when
     given, is (freqs, scale) of qat.rope_freqs: queries and keys are rotated,
     by the row's place in its sequence, or by positions [T] int64 (needed with cu)."""
 
@@ -43,13 +44,22 @@ class CoreAttention:
         return dict(heads=self.heads, kv_heads=self.kv_heads, head_dim=hd, window=self.window,
                     cu_q=self.cu, max_q=self.seq_len, stream=stream)
 
+    def _clear(self, t, stream):
+        """The operators leave rows of no sequence as they are, but the linears and
+        their weight gradients take every row: packed batches start from zero."""
+        if self.cu is not None:
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+                t.zero_()
+
     def forward(self, qkv, att, lse, hd, stream):
         """Rotates qkv in place and writes the attention output and lse."""
+        self._clear(att, stream)
         self.rotate(qkv, hd, False, stream)
         qat.qat_attn_fwd(*self.split(qkv, hd), att, lse, **self._kw(hd, stream))
 
     def backward(self, datt, qkv, att, lse, dqkv, ws, hd, stream):
         """dqkv (of the unrotated projection) from the output's gradient."""
+        self._clear(dqkv, stream)
         qat.qat_attn_bwd(datt, *self.split(qkv, hd), att, lse, *self.split(dqkv, hd), workspace=ws,
                          **self._kw(hd, stream))
         self.rotate(dqkv, hd, True, stream)
@@ -318,12 +328,14 @@ class RecurrentCore:
         return tb["dX"]
 
     def flops(self, T, R):
+        """Of the linears (attention's depend on the sequences)."""
         return 2.0 * T * self.d * (self.nqkv + self.d + 2 * self.H) * R
 
     def flops_bwd(self, T, R):
-        """Contractions of backward(): per application the MLP's four GEMMs
-        (2*T*d*H each) and the O and Q projections' two each (2*T*d*d)."""
-        return (8.0 * T * self.d * self.H + 8.0 * T * self.d * self.d) * R
+        """Contractions of backward()'s linears: per application the MLP's four
+        GEMMs (2*T*d*H each) and the O and Q (with attention Q|K|V) projections' two."""
+        o, qkv = (self.d, self.d) if self.attention is None else (self.W[1].shape[1], self.nqkv)
+        return (8.0 * T * self.d * self.H + 4.0 * T * self.d * (o + qkv)) * R
 
 
 class HeadMlpStep:
@@ -397,7 +409,8 @@ class HeadMlpStep:
 
     def forward_loss(self, X, targets, stream=None):
         """Mean cross entropy of targets [T] int64 (outside [0, vocab): not counted),
-        a device scalar; the losses per token are in self.loss."""
+        a device scalar; the losses per token are in self.loss.  Both are the step's
+        own buffers, which the next call writes again."""
         qe, qf, qp = self.q
         self.loss, lse, mean, ws = self._loss_buffers()
         qat.qat_mlp_fwd(X, self.Z, self.mlp_bits, self.d, self.H, qfc=qf, qproj=qp,
@@ -419,7 +432,8 @@ class HeadMlpStep:
                         workspace=self.ws, stream=stream, act=self.act)
 
     def step_loss(self, X, targets, stream=None, on_head_grad=None):
-        """Quantize, forward, loss, backward: returns the mean loss (a device scalar)."""
+        """Quantize, forward, loss, backward: returns the mean loss (a device scalar
+        that the next step writes again)."""
         self.quantize(stream)
         mean = self.forward_loss(X, targets, stream)
         self.backward_loss(X, targets, stream, on_head_grad)

@@ -105,6 +105,50 @@ def test_core_with_attention(R, window, packed):
         assert fro(got, op.grad) <= bound(R), name
 
 
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_core_rows_behind_the_last_sequence(own_stream):
+    """A packed batch that does not fill its rows, in buffers that held NaN: the rows
+    behind it attend to nothing, and every weight gradient is that of the composition."""
+    d, H, KH, R = 160, 4, 2, 2
+    lens, tail = [100, 33], 27
+    T = sum(lens) + tail
+    pos = torch.cat([torch.arange(n) for n in lens + [tail]])
+    cu = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda")
+    att = steps.CoreAttention(H, KH, max(lens), cu=cu, rope=qat.rope_freqs(24), positions=pos.cuda())
+    core, X = make_core(d, H, KH, 320, T, att)
+    dY = sy.act_bf16(np.random.default_rng(1), T, d, std=sy.DY_STD)
+    tb = core._train_buffers(T, R, "cuda")
+    for n in ("att", "dqkv"):
+        tb[n].fill_(float("nan"))
+    x, dy = X.cuda(), dY.cuda()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream() if own_stream else None
+    out = core.forward_train(x, R, stream=stream)
+    dX = core.backward(dy, stream=stream)
+    torch.cuda.synchronize()
+    assert qat.device_error() == 0
+    kept = out.clone()
+    core.forward(x.clone(), R)
+    core._att[0].fill_(float("nan"))
+    again = core.forward(x.clone(), R)
+    torch.cuda.synchronize()
+    assert torch.equal(kept, again)
+    n = sum(lens)
+    ops = [f64(q.operand).requires_grad_() for q in (core.q_qkv, core.q_o, core.q_fc, core.q_proj)]
+    xr = f64(X).requires_grad_()
+    y = xr
+    for _ in range(R):
+        a = heads_out((y @ ops[0].T)[:n], H, KH, core.hd, lens, att.rope, pos[:n], 0)
+        x1 = y + torch.cat([a, a.new_zeros(tail, d)]) @ ops[1].T
+        y = x1 + (torch.relu(x1 @ ops[2].T) ** 2) @ ops[3].T
+    y.backward(f64(dY))
+    assert fro(kept, y.detach()) <= bound(R)
+    assert fro(dX, xr.grad) <= bound(R)
+    for name, got, op in zip(("dWqkv", "dWo", "dWfc", "dWproj"),
+                             (core.dWqkv, core.dWo, core.dWfc, core.dWproj), ops):
+        assert fro(got, op.grad) <= bound(R), name
+
+
 def test_core_backward_application_and_accumulate_with_attention():
     d, H, KH, T = 160, 4, 4, 130
     att = steps.CoreAttention(H, KH, 65, rope=qat.rope_freqs(40))
