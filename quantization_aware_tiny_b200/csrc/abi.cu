@@ -133,6 +133,19 @@ size_t ce_fwd_bytes(int64_t V, int64_t T) {
 size_t ce_bwd_bytes(int64_t V, int64_t rows) {
   return 2 * align_up(rows * ce_ldg(V) * 2) + align_up(rows * 4);
 }
+// Partial products of dZ where a piece has so few tokens that its tiles leave most of
+// the GPU idle and the reduction over the vocabulary is split (0: it is not).  Loss and
+// gradients (dW's two halves in one product included): one token of 50,000 words, d =
+// 512, 361 -> 103 us; 300 of 20,001, d = 256, 165 -> 71 us; 1,500 of 50,257, d = 768,
+// 689 -> 540 us.
+size_t ce_slab_bytes(int64_t V, int64_t d, int64_t n) {
+  const Slabs s = f32_slabs(n, d, V);
+  return n > 0 && s.count > 1 ? align_up(s.count * s.rows * d * 4) : 0;
+}
+// What every piece of T tokens, `rows` at a time, can use.
+size_t ce_slab_bytes_max(int64_t V, int64_t d, int64_t T, int64_t rows) {
+  return std::max(ce_slab_bytes(V, d, rows), ce_slab_bytes(V, d, T % rows));
+}
 
 // ---- attention
 // The checks that both directions share; fills the kernels' arguments.
@@ -235,7 +248,10 @@ size_t qat_workspace_size(int32_t op, int32_t N_or_d, int32_t K_or_H, int64_t T,
     case QAT_OP_CE_BWD: {  // a = V, b = d; the backward's size serves the forward too
       if (a > kCeMaxVocab || T > kCeMaxTokens) return 0;
       size_t n = T > 0 ? ce_fwd_bytes(a, T) : 0;
-      if (op == QAT_OP_CE_BWD && T > 0) n = std::max(n, ce_bwd_bytes(a, ce_rows_wanted(a, b, T)));
+      if (op == QAT_OP_CE_BWD && T > 0) {
+        const int64_t rows = ce_rows_wanted(a, b, T);
+        n = std::max(n, ce_bwd_bytes(a, rows) + ce_slab_bytes_max(a, b, T, rows));
+      }
       return n + (raw_weights ? operand_bytes(a, b) : 0);
     }
     case QAT_OP_ATTN_BWD:  // a = heads: rowsum(dO * O) of every query and head
@@ -661,6 +677,9 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
   void* glo = ws.take(static_cast<size_t>(rows) * ldg * 2);
   float* rem = static_cast<float*>(ws.take(static_cast<size_t>(rows) * 4));
   if (!ghi || !glo || !rem) return QAT_ERR_WORKSPACE;
+  // (a smaller workspace than asked for may leave no room for these: the product is then whole)
+  const size_t slab_bytes = dZ ? ce_slab_bytes_max(V, d, T, rows) : 0;
+  float* slabs = slab_bytes ? static_cast<float*>(ws.take(slab_bytes)) : nullptr;
   if (dZ == Z) return QAT_ERR_ARG;  // dW reads the rows of Z after their dZ is written
   for (int64_t t0 = 0; t0 < T; t0 += rows) {
     const int64_t n = std::min(rows, T - t0);
@@ -685,26 +704,48 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
       x.A = ghi; x.lda = ldg;
       x.B = op; x.ldb = d; x.b_mn = true;
       x.M = n; x.N = d; x.K = V;
-      x.epi = EPI_CE_DZ;
-      x.D = dZ + t0 * d; x.ldd = d;
-      x.ce.targets = targets + t0;
-      x.ce.vocab = V;
-      x.ce.rem = rem;
-      x.ce.words = op;
-      rc = launch_gemm(x, stream);
+      const Slabs sl = f32_slabs(n, d, V);
+      if (slabs && sl.count > 1) {  // few tokens: over parts of the vocabulary, joined after
+        x.epi = EPI_F32;
+        x.slabs = true;
+        x.D = slabs; x.ldd = d;
+        rc = launch_gemm(x, stream);
+        if (rc) return rc;
+        CeDz j{};
+        j.slabs = slabs;
+        j.count = sl.count;
+        j.rows = sl.rows;
+        j.targets = targets + t0;
+        j.rem = rem;
+        j.words = op;
+        j.dZ = reinterpret_cast<__nv_bfloat16*>(dZ + t0 * d);
+        j.n = n;
+        j.d = d;
+        j.vocab = V;
+        rc = launch_ce_dz_join(j, stream);
+      } else {
+        x.epi = EPI_CE_DZ;
+        x.D = dZ + t0 * d; x.ldd = d;
+        x.ce.targets = targets + t0;
+        x.ce.vocab = V;
+        x.ce.rem = rem;
+        x.ce.words = op;
+        rc = launch_gemm(x, stream);
+      }
       if (rc) return rc;
     }
     // dW (+)= g^T . Z, kept in 32 bits: g's bf16 rounding alone would leave it
-    // 1e-3 off, so its remainder is multiplied too (and first: it is small).
-    for (int half = 0; dW && half < 2; ++half) {
+    // 1e-3 off, so its remainder is multiplied too (and first: it is small), in the same
+    // pass: dW of a large vocabulary is written once, not written, read and written.
+    if (dW) {
       GemmDesc w;
-      w.A = half ? ghi : glo; w.lda = ldg; w.a_mn = true;
+      w.A = glo; w.A2 = ghi; w.lda = ldg; w.a_mn = true;
       w.B = Zp; w.ldb = ldz; w.b_mn = true;
       w.M = V; w.N = d; w.K = n;
       w.epi = EPI_F32;
       w.D = dW; w.ldd = d;
       w.k_run = kCeTokenRun;
-      w.accumulate = accumulate_dW != 0 || t0 > 0 || half > 0;
+      w.accumulate = accumulate_dW != 0 || t0 > 0;
       rc = launch_gemm(w, stream);
       if (rc) return rc;
     }

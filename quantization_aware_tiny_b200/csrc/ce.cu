@@ -107,11 +107,51 @@ __global__ void __launch_bounds__(1024) ce_mean_kernel(const CePart* parts, int6
   }
 }
 
+// The slabs of dZ, four columns a thread, added in their order.  Bound by reading
+// count * n * d floats, which the product has just left in L2 (at most one
+// output tile per CTA: under 20 MB).
+__global__ void __launch_bounds__(256) ce_dz_join_kernel(const CeDz j) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int groups = j.d / 4;
+  if (i >= j.n * groups) return;
+  const int64_t t = i / groups;
+  const int c = static_cast<int>(i - t * groups) * 4;
+  const int64_t y = j.targets[t];
+  const float* p = j.slabs + t * j.d + c;
+  const int64_t step = j.rows * j.d;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int s = 0; s < j.count; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(p + s * step);
+    a.x += v.x;
+    a.y += v.y;
+    a.z += v.z;
+    a.w += v.w;
+  }
+  if (y >= 0 && y < j.vocab) {
+    const float r = j.rem[t];
+    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(j.words + y * j.d + c);
+    const float2 u = __bfloat1622float2(w[0]), v = __bfloat1622float2(w[1]);
+    a = make_float4(fmaf(r, u.x, a.x), fmaf(r, u.y, a.y), fmaf(r, v.x, a.z), fmaf(r, v.y, a.w));
+  }
+  __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(j.dZ + t * j.d + c);
+  o[0] = __floats2bfloat162_rn(a.x, a.y);
+  o[1] = __floats2bfloat162_rn(a.z, a.w);
+}
+
 int64_t join_blocks(int64_t T) { return (T + kJoinRows - 1) / kJoinRows; }
 
 }  // namespace
 
 int64_t ce_parts_bytes(int64_t T) { return join_blocks(T) * static_cast<int64_t>(sizeof(CePart)); }
+
+int launch_ce_dz_join(const CeDz& j, cudaStream_t stream) {
+  const int64_t blocks = (j.n * (j.d / 4) + 255) / 256;
+  if (blocks > (1ll << 31) - 1) return QAT_ERR_SHAPE;
+  ce_dz_join_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(j);
+  count_launch();
+  return cuda_status(cudaGetLastError());
+}
 
 int launch_ce_join(const CeJoin& j, cudaStream_t stream) {
   const int64_t blocks = join_blocks(j.T);

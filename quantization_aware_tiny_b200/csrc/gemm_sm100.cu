@@ -95,6 +95,8 @@ struct KArgs {
   int M, N;
   int num_m_blk, num_n_blk, splits, kblk_total, kblk_per_split, num_tiles;
   int ordered;  // EPI_F32_ATOMIC: one CTA (pair) takes all splits of a tile, in order
+  int kblk_a2;    // fp32 outputs of MN-major operands: k-blocks from here on are A2's (tmR), with B from its start
+  int slab_rows;  // EPI_F32: row distance of the splits' outputs (0: one output)
   void* D;
   int64_t ldd;
   void* D2;
@@ -492,7 +494,14 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
         const int n0 = nb * BN + static_cast<int>(rank) * C::B_ROWS;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) { ok = false; break; }
-          const int k0 = kb * BK;
+          int k0 = kb * BK;
+          const CUtensorMap* ta = &tmA;
+          if constexpr (A_MN && C::F32) {
+            if (kb >= p.kblk_a2) {
+              k0 -= p.kblk_a2 * BK;
+              ta = &tmR;
+            }
+          }
           uint8_t* a_dst = sA + stage * C::A_BYTES;
           uint8_t* b_dst = sB + stage * C::B_BYTES;
           if constexpr (PAIR) {
@@ -502,8 +511,8 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
             if constexpr (!A_MN) {
               tma_load_2d_pair(&tmA, bar, a_dst, k0, m0);
             } else {
-              tma_load_2d_pair(&tmA, bar, a_dst, m0, k0);
-              tma_load_2d_pair(&tmA, bar, a_dst + 64 * 128, m0 + 64, k0);
+              tma_load_2d_pair(ta, bar, a_dst, m0, k0);
+              tma_load_2d_pair(ta, bar, a_dst + 64 * 128, m0 + 64, k0);
             }
             if constexpr (FB) {
               // B comes from the resident panel
@@ -519,8 +528,8 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
             if constexpr (!A_MN) {
               tma_load_2d(&tmA, &full[stage], a_dst, k0, m0);
             } else {
-              tma_load_2d(&tmA, &full[stage], a_dst, m0, k0);
-              tma_load_2d(&tmA, &full[stage], a_dst + 64 * 128, m0 + 64, k0);
+              tma_load_2d(ta, &full[stage], a_dst, m0, k0);
+              tma_load_2d(ta, &full[stage], a_dst + 64 * 128, m0 + 64, k0);
             }
             if constexpr (FB) {
               // B comes from the resident panel
@@ -771,7 +780,11 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
         if (lane == 0) {
           const uint8_t* s0 = staging + (buf0 - smem_u32(staging));
           if constexpr (EPI == EPI_F32_ATOMIC) {
-            tma_reduce_add_2d(&tmD, s0, col0, row0);
+            // (the first of ordered splits writes: nothing has to be cleared before)
+            if (ordered && !p.accumulate && tile_sp(tile) == 0) tma_store_2d(&tmD, s0, col0, row0);
+            else tma_reduce_add_2d(&tmD, s0, col0, row0);
+          } else if constexpr (EPI == EPI_F32) {
+            tma_store_2d(&tmD, s0, col0, row0 + tile_sp(tile) * p.slab_rows);
           } else if constexpr (epi_act_fwd(EPI)) {
             if (keep_pre) tma_store_2d(&tmD, s0, col0, row0);
             tma_store_2d(&tmD2, staging + (buf1 - smem_u32(staging)), col0, row0);
@@ -918,6 +931,7 @@ int dispatch_bn(const GemmDesc& g, const CUtensorMap& ma, const CUtensorMap& mb,
     }
   } else if (!g.a_mn && g.b_mn) {
     switch (epi) {
+      case EPI_F32: return launch_t<BN, false, true, EPI_F32, PAIR>(ma, mb, md, md2, mr, a, s);
       case EPI_BF16: return launch_t<BN, false, true, EPI_BF16, PAIR>(ma, mb, md, md2, mr, a, s);
       case EPI_BF16_RESID:
         return launch_t<BN, false, true, EPI_BF16_RESID, PAIR>(ma, mb, md, md2, mr, a, s);
@@ -1027,6 +1041,19 @@ int64_t ce_slots(int64_t M, int64_t N) {
   return (N + BN - 1) / BN * 2;
 }
 
+Slabs f32_slabs(int64_t M, int64_t N, int64_t K) {
+  int BN;
+  bool pair;
+  choose_tile(M, N, false, false, &BN, &pair);
+  const int64_t tile_m = pair ? 2 * BM : BM, m_blk = (M + tile_m - 1) / tile_m;
+  const int64_t tiles = m_blk * ((N + BN - 1) / BN);
+  const int units = pair ? sm_count() / 2 : sm_count();
+  const int kblk = static_cast<int>((K + BK - 1) / BK);
+  const int s = 2 * tiles >= units ? 1 : choose_splits(static_cast<int>(tiles), kblk, units);
+  const int per = (kblk + s - 1) / s;
+  return Slabs{(kblk + per - 1) / per, m_blk * tile_m};  // no empty split
+}
+
 bool fused_b_supported(int64_t M, int64_t N, int64_t K, int epi) {
   const bool fwd_epi = epi == EPI_BF16 || epi == EPI_BF16_RESID || epi == EPI_RELU2 || epi == EPI_LRELU2;
   return fwd_epi && M >= 256 && N > 0 && K > 0 && (K & 7) == 0 && fused_b_bn(N, K) != 0;
@@ -1057,6 +1084,8 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
   if (((g.N & 7) && g.epi != EPI_CE_STATS && g.epi != EPI_CE_GRAD) || (g.lda & 7) || (g.ldb & 7) || (g.ldd & 7) || (g.D2 && (g.ldd2 & 7)) ||
       (g.R && (g.ldr & 7)))
     return QAT_ERR_SHAPE;
+  if (g.A2 && (!g.a_mn || !g.b_mn || g.epi != EPI_F32 || !aligned16(g.A2))) return QAT_ERR_ARG;
+  if (g.slabs && (g.a_mn || !g.b_mn || g.epi != EPI_F32 || g.accumulate)) return QAT_ERR_ARG;
   if (g.M > (1ll << 31) - 256 || g.N > (1 << 30) || g.K > (1ll << 31) - 256) return QAT_ERR_SHAPE;
 
   int BN;
@@ -1065,7 +1094,7 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
     pair = true;
     BN = fused_b_bn(g.N, g.K);
   } else {
-    choose_tile(g.M, g.N, g.epi == EPI_F32 || g.epi == EPI_F32_ATOMIC, g.a_mn, &BN, &pair);
+    choose_tile(g.M, g.N, (g.epi == EPI_F32 || g.epi == EPI_F32_ATOMIC) && !g.slabs, g.a_mn, &BN, &pair);
   }
   const int tile_m = pair ? 2 * BM : BM;
 
@@ -1075,6 +1104,8 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
   a.num_m_blk = static_cast<int>((g.M + tile_m - 1) / tile_m);
   a.num_n_blk = static_cast<int>((g.N + BN - 1) / BN);
   a.kblk_total = static_cast<int>((g.K + BK - 1) / BK);
+  a.kblk_a2 = a.kblk_total;
+  if (g.A2) a.kblk_total *= 2;
   a.splits = 1;
   a.D = g.D;
   a.ldd = g.ldd;
@@ -1090,7 +1121,15 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
   a.ce = g.ce;
 
   int epi = g.epi;
-  if (epi == EPI_F32 || epi == EPI_F32_ATOMIC) {
+  int64_t d_rows = g.M;
+  if (g.slabs) {
+    const Slabs sl = f32_slabs(g.M, g.N, g.K);
+    a.splits = sl.count;
+    a.kblk_per_split = (a.kblk_total + sl.count - 1) / sl.count;
+    a.slab_rows = static_cast<int>(sl.rows);
+    d_rows = sl.count * sl.rows;
+    if (d_rows > (1ll << 31) - 256) return QAT_ERR_SHAPE;
+  } else if (epi == EPI_F32 || epi == EPI_F32_ATOMIC) {
     const int tiles = a.num_m_blk * a.num_n_blk;
     // Split K only while the output tiles occupy fewer than half the CTAs
     // (pairs): with more tiles, a wave of whole tiles already keeps at least
@@ -1108,7 +1147,7 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
     s = (a.kblk_total + a.kblk_per_split - 1) / a.kblk_per_split;  // no empty split
     a.splits = s;
     if (s > 1 || g.accumulate) {
-      if (!g.accumulate) {
+      if (!g.accumulate && !a.ordered) {
         cudaError_t e = (g.ldd == g.N)
                             ? cudaMemsetAsync(g.D, 0, static_cast<size_t>(g.M * g.N) * 4, stream)
                             : cudaMemset2DAsync(g.D, static_cast<size_t>(g.ldd) * 4, 0,
@@ -1145,7 +1184,7 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
   const void* d_base = g.D ? g.D : g.D2;
   const int64_t d_ld = g.D ? g.ldd : g.ldd2;
   if (g.epi != EPI_CE_STATS) {  // (the statistics have no tiled output)
-    rc = make_out_map(&md, d_base, g.N, g.M, d_ld, f32);
+    rc = make_out_map(&md, d_base, g.N, d_rows, d_ld, f32);
     if (rc) return rc;
     rc = make_out_map(&md2, g.D2 ? g.D2 : d_base, g.N, g.M, g.D2 ? g.ldd2 : d_ld, false);
     if (rc) return rc;
@@ -1153,6 +1192,10 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
   CUtensorMap mr = md;
   if (epi_reads_r(g.epi)) {
     rc = make_out_map(&mr, g.R, g.N, g.M, g.ldr, false);
+    if (rc) return rc;
+  }
+  if (g.A2) {
+    rc = make_map(&mr, g.A2, g.M, g.K, g.lda, 64);
     if (rc) return rc;
   }
   if (g.Wraw) {

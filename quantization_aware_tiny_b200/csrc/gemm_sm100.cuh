@@ -78,6 +78,12 @@ struct GemmDesc {
   // The tensor core's fp32 accumulation truncates at every step, so a sum over
   // very long K drifts; runs are added to D in 32 bits, rounded to nearest.
   int64_t k_run = 0;
+  // fp32 epilogues of MN-major operands: a second A of the same shape and stride,
+  // multiplied with the same B into the same accumulators, D = A^T B + A2^T B.
+  const void* A2 = nullptr;
+  // EPI_F32 with a K-major A: the reduction is split as f32_slabs() says and D holds
+  // the partial products, slab s at row s * rows (added up by the caller's next kernel).
+  bool slabs = false;
   // Fused quantizing B producer: when set, B / ldb are ignored and the kernel
   // builds the bf16 operand bf16(fl32(c * s)) of this fp32 weight [N,K]
   // (row-major, ld = K) on the grid `bits` in shared memory -- the quantized
@@ -90,6 +96,14 @@ struct GemmDesc {
 
 // Partial statistics per row that EPI_CE_STATS writes for an M x N product.
 int64_t ce_slots(int64_t M, int64_t N);
+
+// Slabs that the product of `slabs` writes: count (1: the output's tiles alone occupy
+// half the CTAs or pairs, a split would not pay) and rows of each.
+struct Slabs {
+  int count;
+  int64_t rows;
+};
+Slabs f32_slabs(int64_t M, int64_t N, int64_t K);
 
 // Whether launch_gemm can quantize B inside the GEMM for this shape / epilogue.
 bool fused_b_supported(int64_t M, int64_t N, int64_t K, int epi);

@@ -23,6 +23,21 @@ struct CeJoin {
 int64_t ce_parts_bytes(int64_t T);
 int launch_ce_join(const CeJoin& j, cudaStream_t stream);
 
+// ---- cross entropy, few tokens: dZ = bf16(sum of the product's slabs + rem *
+// the target's row of the operand)
+struct CeDz {
+  const float* slabs;  // [count][rows][d]
+  int count;
+  int64_t rows;
+  const int64_t* targets;  // [n]
+  const float* rem;        // [n], read where the row has a target
+  const __nv_bfloat16* words;  // [vocab, d]
+  __nv_bfloat16* dZ;           // [n, d]
+  int64_t n;
+  int d, vocab;
+};
+int launch_ce_dz_join(const CeDz& j, cudaStream_t stream);
+
 // ---- rotary positions (row strides in elements; Y may equal X)
 struct RopeArgs {
   const void* X;

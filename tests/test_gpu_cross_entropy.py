@@ -251,3 +251,35 @@ def test_ce_long_sum_over_tokens():
     a, b = run(c, V, d), run(c, V, d)
     check(c, V, d, a)
     assert torch.equal(a[4], b[4])
+
+
+@pytest.mark.parametrize("shape", [(1, 20001, 264), (40, 9000, 64), (300, 20001, 136), (1000, 5003, 512)])
+def test_ce_few_tokens_of_many_words(shape):
+    """dZ's reduction over the vocabulary is split and joined in order: the formula's
+    values, the same bits twice, and with a workspace that has no room for the parts."""
+    T, V, d = shape
+    c = make(T, V, d, seed=T, ignored=0.1 if T > 1 else 0.0)
+    got = run(c, V, d)
+    check(c, V, d, got)
+    assert all(torch.equal(a, b) for a, b in zip(got[:4], run(c, V, d)[:4]))
+    small = torch.empty(4 * T * ((V + 7) // 8 * 8) + 4 * T + 1024, dtype=torch.uint8, device="cuda")
+    assert small.numel() < qat.workspace_size(qat.QAT_OP_CE_BWD, V, d, T, False)
+    check(c, V, d, run(c, V, d, ws=small))
+
+
+@pytest.mark.parametrize("T", [1000, 1100])
+def test_ce_runs_of_tokens_added_in_order(T):
+    """As many output tiles as fill the GPU: dW's runs of tokens are added by one CTA
+    pair, the first written over what was there; the same bits twice."""
+    V, d = 10008, 256
+    c = make(T, V, d, seed=T, ignored=0.1)
+    got = run(c, V, d)
+    check(c, V, d, got)
+    assert torch.equal(got[4], run(c, V, d)[4])
+    dW = got[4].clone()
+    ws = workspace(qat.QAT_OP_CE_BWD, V, d, T)
+    qat.qat_ce_bwd(c["Zd"], c["td"], got[1], 8, qw=c["q"], gscale=got[2][1:], dW=dW, accumulate_dW=True, workspace=ws)
+    torch.cuda.synchronize()
+    # the runs (at most 2, each within twice the largest sum M) added to the first sum: adds
+    # of at most M, 3 M and 2 M, each off by at most half a step, 2^-24
+    assert bool(((dW - 2 * got[4]).abs() <= 6 * 2 ** -24 * got[4].abs().max()).all())
