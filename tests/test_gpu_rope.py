@@ -48,6 +48,18 @@ def test_rope_heads_and_parts(dims, interleaved, dtype):
     check(37, 3, hd, rot, dtype, interleaved, True, far=5000, in_place=True, pad=8)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dims", [(72, 30, 7), (80, 20, 5), (128, 10, 16), (40, 34, 1), (1024, 1022, 2), (2056, 1018, 2),
+                                  (8, 2, 300)])
+def test_rope_parts_that_end_inside_a_pack(dims, interleaved, dtype):
+    """Halves off the 16-byte packs, rotated parts that end inside one, more packs than a
+    block has threads, rows of no token's multiple, in and out of place."""
+    hd, rot, heads = dims
+    check(29, heads, hd, rot, dtype, interleaved, False, far=5000, pad=8, in_place=True)
+    check(29, heads, hd, rot, dtype, interleaved, True, far=5000, pad=16)
+
+
 @pytest.mark.parametrize("T", [1, 2, 63, 1000, 4097])
 def test_rope_lengths_and_wrapped_rows(T):
     check(T, 12, 64, 64, BF, False, False, given=False, seq_len=100)
