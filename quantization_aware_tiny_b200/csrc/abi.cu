@@ -135,9 +135,9 @@ size_t ce_bwd_bytes(int64_t V, int64_t rows) {
 }
 // Partial products of dZ where a piece has so few tokens that its tiles leave most of
 // the GPU idle and the reduction over the vocabulary is split (0: it is not).  Loss and
-// gradients (dW's two halves in one product included): one token of 50,000 words, d =
-// 512, 361 -> 103 us; 300 of 20,001, d = 256, 165 -> 71 us; 1,500 of 50,257, d = 768,
-// 689 -> 540 us.
+// gradients (dW's two halves in one product and the joins included): one token of 50,000
+// words, d = 512, 361 -> 89 us; 300 of 20,001, d = 256, 165 -> 66 us; 1,500 of 50,257,
+// d = 768, 689 -> 544 us.
 size_t ce_slab_bytes(int64_t V, int64_t d, int64_t n) {
   const Slabs s = f32_slabs(n, d, V);
   return n > 0 && s.count > 1 ? align_up(s.count * s.rows * d * 4) : 0;

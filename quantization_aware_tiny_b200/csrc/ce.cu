@@ -13,7 +13,13 @@ namespace {
 constexpr int kJoinRows = 32;   // tokens of a block: one per lane, so the pairs load coalesced
 constexpr int kJoinWarps = 32;  // most warps of a block; slots are dealt to them in turn
 
-// (sum of losses, counted tokens) of a block of kJoinRows tokens.
+// Up to this many tokens a block joins a single one, its lanes taking the slots: a
+// block of 32 tokens would leave most of the GPU idle and walk the slots one after
+// another (loss and gradients of one token of 50,000 words, d = 512: 103 -> 89 us with
+// the slabs' join by parts; 130 tokens of 1,024 words: 42.6 -> 40 us).
+constexpr int64_t kJoinSingle = 1024;
+
+// (sum of losses, counted tokens) of a block's tokens.
 struct alignas(16) CePart {
   double sum;
   int64_t count;
@@ -70,6 +76,34 @@ __global__ void __launch_bounds__(kJoinRows* kJoinWarps) ce_join_kernel(const Ce
   if (lane == 0) static_cast<CePart*>(j.parts)[blockIdx.x] = CePart{sum, count};
 }
 
+// The same for one token per block, a lane taking every blockDim.x-th slot.
+__global__ void __launch_bounds__(256) ce_join_single_kernel(const CeJoin j) {
+  __shared__ float2 part[8];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t t = blockIdx.x;
+  float m = -INFINITY, s = 0.0f;
+  for (int i = threadIdx.x; i < j.slots; i += blockDim.x) {
+    const float2 v = j.stats[i * j.T + t];
+    merge_stats(m, s, v.x, v.y);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_down_sync(0xffffffffu, m, o), s2 = __shfl_down_sync(0xffffffffu, s, o);
+    merge_stats(m, s, m2, s2);
+  }
+  if (lane == 0) part[w] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int i = 1; i < warps; ++i) merge_stats(m, s, part[i].x, part[i].y);
+  const float lse = m + logf(s);
+  const int64_t y = j.targets[t];
+  const bool counted = y >= 0 && y < j.vocab;
+  const float loss = counted ? lse - j.tlogit[t] : 0.0f;
+  j.lse[t] = lse;
+  j.loss[t] = loss;
+  if (j.mean) static_cast<CePart*>(j.parts)[t] = CePart{loss, counted};
+}
+
 // Mean loss over the counted tokens: the blocks' sums in 64 bits and in a fixed
 // order, so the same inputs always give the same bits.
 __global__ void __launch_bounds__(1024) ce_mean_kernel(const CePart* parts, int64_t n, float* mean) {
@@ -107,27 +141,34 @@ __global__ void __launch_bounds__(1024) ce_mean_kernel(const CePart* parts, int6
   }
 }
 
-// The slabs of dZ, four columns a thread, added in their order.  Bound by reading
-// count * n * d floats, which the product has just left in L2 (at most one
+// The slabs of dZ: a block takes 128 columns of a token, four a thread; blockDim.y
+// threads share a column's slabs and the first adds their sums in order.  Bound by
+// reading count * n * d floats, which the product has just left in L2 (at most one
 // output tile per CTA: under 20 MB).
-__global__ void __launch_bounds__(256) ce_dz_join_kernel(const CeDz j) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int groups = j.d / 4;
-  if (i >= j.n * groups) return;
-  const int64_t t = i / groups;
-  const int c = static_cast<int>(i - t * groups) * 4;
-  const int64_t y = j.targets[t];
-  const float* p = j.slabs + t * j.d + c;
-  const int64_t step = j.rows * j.d;
+constexpr int kDzParts = 8;
+__global__ void __launch_bounds__(32 * kDzParts) ce_dz_join_kernel(const CeDz j) {
+  __shared__ float4 part[kDzParts][32];
+  const int64_t t = blockIdx.x;
+  const int c = (blockIdx.y * 32 + threadIdx.x) * 4;
+  const bool live = c < j.d;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-  for (int s = 0; s < j.count; ++s) {
-    const float4 v = *reinterpret_cast<const float4*>(p + s * step);
+  auto add = [&](const float4& v) {
     a.x += v.x;
     a.y += v.y;
     a.z += v.z;
     a.w += v.w;
+  };
+  if (live) {
+    const float* p = j.slabs + t * j.d + c;
+    const int64_t step = j.rows * j.d;
+#pragma unroll 8
+    for (int s = threadIdx.y; s < j.count; s += blockDim.y) add(*reinterpret_cast<const float4*>(p + s * step));
   }
+  part[threadIdx.y][threadIdx.x] = a;
+  __syncthreads();
+  if (threadIdx.y != 0 || !live) return;
+  for (int i = 1; i < static_cast<int>(blockDim.y); ++i) add(part[i][threadIdx.x]);
+  const int64_t y = j.targets[t];
   if (y >= 0 && y < j.vocab) {
     const float r = j.rem[t];
     const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(j.words + y * j.d + c);
@@ -139,16 +180,17 @@ __global__ void __launch_bounds__(256) ce_dz_join_kernel(const CeDz j) {
   o[1] = __floats2bfloat162_rn(a.z, a.w);
 }
 
-int64_t join_blocks(int64_t T) { return (T + kJoinRows - 1) / kJoinRows; }
+int64_t join_blocks(int64_t T) { return T <= kJoinSingle ? T : (T + kJoinRows - 1) / kJoinRows; }
 
 }  // namespace
 
 int64_t ce_parts_bytes(int64_t T) { return join_blocks(T) * static_cast<int64_t>(sizeof(CePart)); }
 
 int launch_ce_dz_join(const CeDz& j, cudaStream_t stream) {
-  const int64_t blocks = (j.n * (j.d / 4) + 255) / 256;
-  if (blocks > (1ll << 31) - 1) return QAT_ERR_SHAPE;
-  ce_dz_join_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(j);
+  const int64_t columns = (j.d + 127) / 128;
+  if (j.n > (1ll << 31) - 1 || columns > 65535) return QAT_ERR_SHAPE;
+  const int parts = std::min(kDzParts, (j.count + 3) / 4);  // four slabs a thread or more
+  ce_dz_join_kernel<<<dim3(static_cast<unsigned>(j.n), static_cast<unsigned>(columns)), dim3(32, parts), 0, stream>>>(j);
   count_launch();
   return cuda_status(cudaGetLastError());
 }
@@ -158,7 +200,10 @@ int launch_ce_join(const CeJoin& j, cudaStream_t stream) {
   // about 8 slots a warp: 64 slots (8,192 words) 8 warps, 394 (50,257 words) 32, where 8
   // warps took 25 us for 4,099 tokens
   const int warps = std::min(kJoinWarps, std::max(1, (j.slots + 7) / 8));
-  ce_join_kernel<<<static_cast<unsigned>(blocks), kJoinRows * warps, 0, stream>>>(j);
+  if (j.T <= kJoinSingle)
+    ce_join_single_kernel<<<static_cast<unsigned>(blocks), std::min(256, (j.slots + 31) / 32 * 32), 0, stream>>>(j);
+  else
+    ce_join_kernel<<<static_cast<unsigned>(blocks), kJoinRows * warps, 0, stream>>>(j);
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return QAT_ERR_CUDA;
