@@ -153,7 +153,7 @@ def _p(t):
 def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ws(ws):
@@ -385,7 +385,7 @@ _FLOAT = {torch.float32: "fp32", torch.bfloat16: "bf16"}
 def _need(where, *specs):
     """Refuses what the C side cannot see from a pointer: specs are (tensor or
     None, dtype, elements at least); every tensor on the current CUDA device."""
-    cur = torch.cuda.current_device()
+    cur = torch._C._cuda_getDevice()
     for t, dtype, n in specs:
         if t is not None and (t.dtype is not dtype or t.get_device() != cur or t.numel() < n):
             raise QatError(QAT_ERR_ARG, where)
