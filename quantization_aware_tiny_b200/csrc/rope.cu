@@ -72,9 +72,9 @@ struct FastDiv {
 // are copied, unless Y is X.
 //
 // Measured, 12 heads: 65,536 tokens of 64 bf16, halves 34.2 us (5.9 TB/s), interleaved
-// 41.8; 16,383 tokens of 64 fp32, 16 dims interleaved 19.3 us (5.2 TB/s).  Where a part
+// 40.3; 16,383 tokens of 64 fp32, 16 dims interleaved 19.1 us (5.3 TB/s).  Where a part
 // ends off a pack, against loads and stores of single elements: 65,536 tokens of 72,
-// 30 dims in halves 245 -> 58 us, 40,000 of 80, 20 dims interleaved 88 -> 33 us.  More
+// 30 dims in halves 245 -> 58 us, 40,000 of 80, 20 dims interleaved 88 -> 32 us.  More
 // packs of a thread in flight, 2 to 8, gave nothing.
 enum Layout : int { kPairs, kHalves, kAcross };
 
@@ -82,9 +82,9 @@ template <class T, Layout L>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs r, int tokens_per_block, const FastDiv by_token,
                                                         const FastDiv by_head) {
   constexpr int W = 16 / sizeof(T);
-  __shared__ float2 table[kTablePairs];
+  __shared__ alignas(16) float2 table[kTablePairs];  // rows of an even number of pairs: two are read at once
   __shared__ Pack<T> staged[L == kAcross ? kThreads : 1];
-  const int pairs = r.rotary >> 1;
+  const int pairs = r.rotary >> 1, stride = (pairs + 1) & ~1;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block;
   const int nt = static_cast<int>(min(static_cast<int64_t>(tokens_per_block), r.T - t0));
   for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs r, int to
     const double turns = static_cast<double>(pos) * r.freqs[k];
     float s, c;
     sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &c);
-    table[i] = make_float2(c * r.scale, (r.inverse ? -s : s) * r.scale);
+    table[t * stride + k] = make_float2(c * r.scale, (r.inverse ? -s : s) * r.scale);
   }
   __syncthreads();
   const int units = static_cast<int>(by_head.d), per_token = static_cast<int>(by_token.d);
@@ -111,17 +111,23 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs r, int to
     const int64_t at = static_cast<int64_t>(h) * r.head_dim;
     const T* x = X + t * r.ldx + at;
     T* y = Y + t * r.ldy + at;
-    const float2* tab = table + t * pairs;
+    const float2* tab = table + t * stride;
     if constexpr (L == kPairs) {
       Pack<T> a = load(x + u * W);
 #pragma unroll
-      for (int e = 0; e < W; e += 2) {
+      for (int e = 0; e < W; e += 4) {
         const int k = (u * W + e) >> 1;
         if (k < pairs) {
-          const float2 cs = tab[k];
-          const float p = to_f(a.v[e]), q = to_f(a.v[e + 1]);
+          const float4 cs = *reinterpret_cast<const float4*>(tab + k);
+          float p = to_f(a.v[e]), q = to_f(a.v[e + 1]);
           a.v[e] = from_f<T>(p * cs.x - q * cs.y);
           a.v[e + 1] = from_f<T>(p * cs.y + q * cs.x);
+          if (k + 1 < pairs) {
+            p = to_f(a.v[e + 2]);
+            q = to_f(a.v[e + 3]);
+            a.v[e + 2] = from_f<T>(p * cs.z - q * cs.w);
+            a.v[e + 3] = from_f<T>(p * cs.w + q * cs.z);
+          }
         }
       }
       store(y + u * W, a);
@@ -133,11 +139,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs r, int to
       }
       Pack<T> a = load(x + u * W), b = load(x + pairs + u * W);
 #pragma unroll
-      for (int e = 0; e < W; ++e) {
-        const float2 cs = tab[u * W + e];
-        const float p = to_f(a.v[e]), q = to_f(b.v[e]);
+      for (int e = 0; e < W; e += 2) {
+        const float4 cs = *reinterpret_cast<const float4*>(tab + u * W + e);
+        const float p = to_f(a.v[e]), q = to_f(b.v[e]), v = to_f(a.v[e + 1]), w = to_f(b.v[e + 1]);
         a.v[e] = from_f<T>(p * cs.x - q * cs.y);
         b.v[e] = from_f<T>(p * cs.y + q * cs.x);
+        a.v[e + 1] = from_f<T>(v * cs.z - w * cs.w);
+        b.v[e + 1] = from_f<T>(v * cs.w + w * cs.z);
       }
       store(y + u * W, a);
       store(y + pairs + u * W, b);
@@ -179,7 +187,7 @@ int launch(const RopeArgs& r, cudaStream_t s) {
   // enough rows for a few packs per thread, a table that fits, and blocks for every SM
   const int64_t row_units = static_cast<int64_t>(r.heads) * r.head_dim / W;
   int64_t tok = std::max<int64_t>(1, 4 * kThreads / std::max<int64_t>(1, row_units));
-  tok = std::min<int64_t>(tok, std::max(1, kTablePairs / std::max(1, pairs)));
+  tok = std::min<int64_t>(tok, std::max(1, kTablePairs / (pairs + 1)));
   const int64_t blocks = (r.T + tok - 1) / tok;
   if (blocks > (1ll << 31) - 1) return QAT_ERR_SHAPE;
   const int rotated = (r.rotary + W - 1) / W;
