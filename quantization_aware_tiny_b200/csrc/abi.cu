@@ -127,8 +127,12 @@ int64_t ce_rows_wanted(int64_t V, int64_t d, int64_t T) {
   return std::min<int64_t>(std::max<int64_t>(rows, 256), T);
 }
 
+// (Fewer than 256 tokens may take narrower tiles, hence more statistics each: a workspace
+// of the longest batch serves the shorter ones.)
 size_t ce_fwd_bytes(int64_t V, int64_t T) {
-  return align_up(ce_slots(T, V) * T * 8) + align_up(T * 4) + align_up(ce_parts_bytes(T));
+  const int64_t few = std::min<int64_t>(T, 255);
+  return align_up(std::max(ce_slots(T, V) * T, ce_slots(few, V) * few) * 8) + align_up(T * 4) +
+         align_up(ce_parts_bytes(T));
 }
 size_t ce_bwd_bytes(int64_t V, int64_t rows) {
   return 2 * align_up(rows * ce_ldg(V) * 2) + align_up(rows * 4);

@@ -143,8 +143,8 @@ __global__ void __launch_bounds__(1024) ce_mean_kernel(const CePart* parts, int6
 
 // The slabs of dZ: a block takes 128 columns of a token, four a thread; blockDim.y
 // threads share a column's slabs and the first adds their sums in order.  Bound by
-// reading count * n * d floats, which the product has just left in L2 (at most one
-// output tile per CTA: under 20 MB).
+// reading count * n * d floats, which the product has just left in L2 (one output tile
+// per CTA or pair, under 20 MB, or the few that fill its waves better).
 constexpr int kDzParts = 8;
 __global__ void __launch_bounds__(32 * kDzParts) ce_dz_join_kernel(const CeDz j) {
   __shared__ float4 part[kDzParts][32];
@@ -184,7 +184,10 @@ int64_t join_blocks(int64_t T) { return T <= kJoinSingle ? T : (T + kJoinRows - 
 
 }  // namespace
 
-int64_t ce_parts_bytes(int64_t T) { return join_blocks(T) * static_cast<int64_t>(sizeof(CePart)); }
+// (never less than fewer tokens need: a workspace of the longest batch serves the others)
+int64_t ce_parts_bytes(int64_t T) {
+  return std::max(join_blocks(T), std::min(T, kJoinSingle)) * static_cast<int64_t>(sizeof(CePart));
+}
 
 int launch_ce_dz_join(const CeDz& j, cudaStream_t stream) {
   const int64_t columns = (j.d + 127) / 128;

@@ -75,7 +75,8 @@ struct FastDiv {
 // 40.3; 16,383 tokens of 64 fp32, 16 dims interleaved 19.1 us (5.3 TB/s).  Where a part
 // ends off a pack, against loads and stores of single elements: 65,536 tokens of 72,
 // 30 dims in halves 245 -> 58 us, 40,000 of 80, 20 dims interleaved 88 -> 32 us.  More
-// packs of a thread in flight, 2 to 8, gave nothing.
+// packs of a thread in flight gave nothing (halves, 2 to 8) or lost (interleaved, 2:
+// 40.3 -> 44.4 us).
 enum Layout : int { kPairs, kHalves, kAcross };
 
 template <class T, Layout L>

@@ -71,6 +71,12 @@ def test_ce_workspace_sizes():
     assert qat.workspace_size(qat.QAT_OP_CE_FWD, 64, 64, 0, False) == 0
 
 
+def test_ce_workspace_of_the_longest_batch_serves_shorter_ones():
+    for V, d in ((64, 64), (1024, 512), (50257, 640)):
+        sizes = [qat.workspace_size(qat.QAT_OP_CE_FWD, V, d, T, False) for T in range(1, 2100)]
+        assert sizes == sorted(sizes)
+
+
 # ------------------------------------------------------------------- rotary
 
 def rope(X=A16, ldx=0, Y=ctypes.c_void_p(0x20000), ldy=0, dtype=1, T=4, heads=2, hd=64, rot=64, freqs=A16,
