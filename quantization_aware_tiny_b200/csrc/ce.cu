@@ -26,10 +26,14 @@ struct alignas(16) CePart {
 };
 
 // (m, s) <- the statistics of both halves: s = sum of exp(l - m) over both.
-// m = -inf marks an empty half (s = 0).
+// m = -inf: no logit above -inf; s is then 0, or NaN where logits are (fmaxf passes them
+// over, so the sum carries them).
 __device__ __forceinline__ void merge_stats(float& m, float& s, float m2, float s2) {
   const float t = fmaxf(m, m2);
-  if (t == -INFINITY) return;
+  if (t == -INFINITY) {
+    s += s2;
+    return;
+  }
   s = s * expf(m - t) + s2 * expf(m2 - t);
   m = t;
 }

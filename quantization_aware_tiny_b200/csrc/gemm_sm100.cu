@@ -154,7 +154,7 @@ __device__ __forceinline__ void ce_stats_chunk(const KArgs& p, uint32_t (&acc)[3
 #pragma unroll
   for (int j = 4; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
   const float m = fmaxf(c.m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-  const float m2 = m * kLog2e;
+  const float m2 = m == -INFINITY ? 0.0f : m * kLog2e;  // (-inf - -inf is no probability; NaN stays in the sum)
   const float2 l2 = make_float2(kLog2e, kLog2e), nm = make_float2(-m2, -m2);
   float2 sum[2] = {make_float2(c.s * exp2_fast(fmaf(c.m, kLog2e, -m2)), 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
