@@ -81,18 +81,23 @@ bool bits_ok(int bits) { return bits == 5 || bits == 6 || bits == 8; }
 bool act_ok(int act) { return act == QAT_ACT_RELU2 || act == QAT_ACT_LEAKY_RELU2; }
 bool dim_ok(int64_t x) { return x > 0 && (x & 7) == 0 && x <= (1 << 20); }
 
+// Exactly one of W / qw, of the expected shape.
+int check_operand(const float* W, const qat_qweight* qw, int64_t N, int64_t K) {
+  if ((W == nullptr) == (qw == nullptr)) return QAT_ERR_ARG;
+  if (!qw) return aligned16(W) ? QAT_OK : QAT_ERR_ALIGN;
+  if (!qw->operand || qw->N != N || qw->K != K) return QAT_ERR_ARG;
+  return aligned16(qw->operand) ? QAT_OK : QAT_ERR_ALIGN;
+}
+
 // The bf16 operand of a weight: taken from `qw`, or produced from fp32 `W`
-// into the workspace.  Exactly one of W / qw must be given.
+// into the workspace.
 int get_operand(const float* W, const qat_qweight* qw, int64_t N, int64_t K, int bits, Carver& ws,
                 cudaStream_t s, const __nv_bfloat16** out) {
-  if ((W == nullptr) == (qw == nullptr)) return QAT_ERR_ARG;
+  if (const int rc = check_operand(W, qw, N, K)) return rc;
   if (qw) {
-    if (!qw->operand || qw->N != N || qw->K != K) return QAT_ERR_ARG;
-    if (!aligned16(qw->operand)) return QAT_ERR_ALIGN;
     *out = reinterpret_cast<const __nv_bfloat16*>(qw->operand);
     return QAT_OK;
   }
-  if (!aligned16(W)) return QAT_ERR_ALIGN;
   void* op = ws.take(N * K * 2);
   void* sc = ws.take(N * 4);
   if (!op || !sc) return QAT_ERR_WORKSPACE;
@@ -104,6 +109,9 @@ int get_operand(const float* W, const qat_qweight* qw, int64_t N, int64_t K, int
 }
 
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Longest row stride in bf16 elements (the tensor maps' stride field).
+constexpr int64_t kMaxStride = 1ll << 38;
 
 // ---- softmax cross entropy
 constexpr int64_t kCeMaxVocab = 1 << 20;
@@ -172,7 +180,7 @@ int attn_args(const qat_attn* a, const qat_bf16* Q, const qat_bf16* K, const qat
   const int64_t ldk = a->ldk ? a->ldk : wk, ldv = a->ldv ? a->ldv : wk;
   if (ldq < wq || ldo < wq || ldk < wk || ldv < wk || ((ldq | ldo | ldk | ldv) & 7))
     return QAT_ERR_SHAPE;
-  if (std::max({ldq, ldo, ldk, ldv}) > (1ll << 38)) return QAT_ERR_SHAPE;  // the maps' stride field
+  if (std::max({ldq, ldo, ldk, ldv}) > kMaxStride) return QAT_ERR_SHAPE;
   if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O)) return QAT_ERR_ALIGN;
   if (!aligned_to(lse, 4) || !aligned_to(a->cu_q, 4) || !aligned_to(a->cu_k, 4)) return QAT_ERR_ALIGN;
   AttnArgs p{};
@@ -605,7 +613,7 @@ int qat_ce_fwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
   if ((W == nullptr) == (qw == nullptr)) return QAT_ERR_ARG;
   if (!dim_ok(d) || V > kCeMaxVocab || T > kCeMaxTokens) return QAT_ERR_SHAPE;
   if (ldz == 0) ldz = d;
-  if (ldz < d || (ldz & 7)) return QAT_ERR_SHAPE;
+  if (ldz < d || (ldz & 7) || ldz > kMaxStride) return QAT_ERR_SHAPE;
   if (!aligned_to(targets, 8) || !aligned_to(loss, 4) || !aligned_to(lse, 4) || !aligned_to(mean, 4))
     return QAT_ERR_ALIGN;
   if (T == 0)
@@ -651,7 +659,7 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
   if ((W == nullptr) == (qw == nullptr)) return QAT_ERR_ARG;
   if (!dim_ok(d) || V > kCeMaxVocab || T > kCeMaxTokens) return QAT_ERR_SHAPE;
   if (ldz == 0) ldz = d;
-  if (ldz < d || (ldz & 7)) return QAT_ERR_SHAPE;
+  if (ldz < d || (ldz & 7) || ldz > kMaxStride) return QAT_ERR_SHAPE;
   if (!aligned_to(targets, 8) || !aligned_to(lse, 4) || !aligned_to(dloss, 4) ||
       !aligned_to(gscale, 4))
     return QAT_ERR_ALIGN;
@@ -663,10 +671,11 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
     return QAT_OK;
   }
   if (!aligned16(Z) || !aligned16(workspace)) return QAT_ERR_ALIGN;
-  Carver ws(workspace, ws_bytes);
-  const __nv_bfloat16* op = nullptr;
-  int rc = get_operand(W, qw, V, d, bits, ws, stream, &op);
+  int rc = check_operand(W, qw, V, d);
   if (rc) return rc;
+  Carver ws(workspace, ws_bytes);
+  Carver operand_ws = ws;  // its place comes first; it is filled once nothing is left to refuse
+  if (W) ws.used += operand_bytes(V, d);
   // Tokens of a piece: what the operator asks for, or what the workspace holds
   // (whole row tiles), down to one of them.
   const int64_t ldg = ce_ldg(V);
@@ -685,6 +694,9 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
   const size_t slab_bytes = dZ ? ce_slab_bytes_max(V, d, T, rows) : 0;
   float* slabs = slab_bytes ? static_cast<float*>(ws.take(slab_bytes)) : nullptr;
   if (dZ == Z) return QAT_ERR_ARG;  // dW reads the rows of Z after their dZ is written
+  const __nv_bfloat16* op = nullptr;
+  rc = get_operand(W, qw, V, d, bits, operand_ws, stream, &op);
+  if (rc) return rc;
   for (int64_t t0 = 0; t0 < T; t0 += rows) {
     const int64_t n = std::min(rows, T - t0);
     const qat_bf16* Zp = Z + t0 * ldz;
@@ -854,7 +866,7 @@ int qat_attn_bwd(const qat_attn* a, const qat_bf16* dO, int64_t lddo, const qat_
   p.lddk = lddk ? lddk : wk;
   p.lddv = lddv ? lddv : wk;
   if (p.lddo < wq || p.lddq < wq || p.lddk < wk || p.lddv < wk ||
-      ((p.lddo | p.lddq | p.lddk | p.lddv) & 7) || p.lddo > (1ll << 38))
+      ((p.lddo | p.lddq | p.lddk | p.lddv) & 7) || p.lddo > kMaxStride)
     return QAT_ERR_SHAPE;
   if (!aligned16(dO) || !aligned16(dQ) || !aligned16(dK) || !aligned16(dV) || !aligned16(workspace))
     return QAT_ERR_ALIGN;
