@@ -218,6 +218,8 @@ int qat_mlp_bwd(const float* Wfc, const float* Wproj, const qat_qweight* qfc,
  * -100, say) counts for nothing -- loss 0, gradient 0; its lse is written.
  * loss, lse [T] fp32.  mean (nullable, 2 floats): the mean loss over the
  * counted tokens and 1 / their number (0 and 0 when there are none).
+ * Outputs and the part of the workspace in use share no memory with inputs or one
+ * another (QAT_ERR_ARG, here and in the calls below).
  * Z holds finite values in every row (a NaN of a row without target would reach
  * dW: its zero gradient is multiplied with the row).  Statistics are fp32, the
  * mean's sum fp64; the same inputs give the same bits.  workspace: qat_workspace_size(QAT_OP_CE_FWD, V, d, T, raw) bytes.
@@ -243,7 +245,7 @@ int qat_ce_fwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
  * bytes give the pieces that run fastest and also serve qat_ce_fwd; less works
  * with smaller pieces, down to 256 tokens (1024 bytes per word, V rounded up
  * to a multiple of 8, and 1 KiB beside the operand), below which QAT_ERR_WORKSPACE is
- * returned.  dZ and dW must not overlap Z.  With T = 0, dW is zeroed unless accumulate_dW. */
+ * returned.  With T = 0, dW is zeroed unless accumulate_dW. */
 int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int32_t bits,
                const qat_bf16* Z, int64_t ldz, int64_t T, const int64_t* targets, const float* lse,
                const float* dloss, const float* gscale, qat_bf16* dZ, float* dW,
@@ -259,8 +261,8 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
  * X, Y [T, heads * head_dim] fp32 or bf16 (dtype), rows ldx / ldy elements
  * apart (multiples of 8; 0 -> heads * head_dim): the heads may be a column
  * range of a wider row, such as the query and key columns of a Q|K|V
- * projection.  Y may be X itself (same stride); otherwise they must not
- * overlap.  head_dim a multiple of 8; rotary even, at most head_dim and
+ * projection.  Y may be X itself (same stride); otherwise they share
+ * no elements (columns of one wider row are fine).  head_dim a multiple of 8; rotary even, at most head_dim and
  * QAT_ROPE_MAX_DIMS.  positions [T] int64 (any value), or NULL: row t is at
  * t mod seq_len, or at t with seq_len = 0.  freqs [rotary / 2] fp64, turns per
  * position: angles are reduced to a part of a turn in fp64, so far positions

@@ -3,7 +3,9 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
+#include <numeric>
 
 #include "gemm_sm100.cuh"
 #include "lm_ops.cuh"
@@ -81,12 +83,62 @@ bool bits_ok(int bits) { return bits == 5 || bits == 6 || bits == 8; }
 bool act_ok(int act) { return act == QAT_ACT_RELU2 || act == QAT_ACT_LEAKY_RELU2; }
 bool dim_ok(int64_t x) { return x > 0 && (x & 7) == 0 && x <= (1 << 20); }
 
+// An argument's memory: `rows` runs of `run` bytes, `step` bytes apart (step >= run
+// where there is more than one).  Null or empty ones share nothing.
+struct Span {
+  uintptr_t at;
+  int64_t rows, step, run;
+  Span(const void* p, int64_t n, int64_t step_bytes, int64_t run_bytes)
+      : at(reinterpret_cast<uintptr_t>(p)), rows(n), step(step_bytes), run(run_bytes) {}
+  Span(const void* p, int64_t bytes) : Span(p, 1, bytes, bytes) {}
+  bool empty() const { return !at || rows <= 0 || run <= 0; }
+  uintptr_t end() const { return at + static_cast<uintptr_t>((rows - 1) * step + run); }
+};
+Span rows_span(const qat_bf16* p, int64_t rows, int64_t ld, int64_t cols) { return Span(p, rows, ld * 2, cols * 2); }
+
+// Whether both hold some byte.  Columns of one wider row lie between one another's
+// runs and share none.
+bool shares(const Span& a, const Span& b) {
+  if (a.empty() || b.empty() || a.end() <= b.at || b.end() <= a.at) return false;
+  // A row of a that starts within b hits by its offset modulo b's step, which repeats after
+  // step / gcd rows of a; one that starts before b and reaches it hits.
+  const int64_t first = a.at >= b.at ? 0 : static_cast<int64_t>(b.at - a.at) / a.step;
+  const int64_t last = std::min(a.rows - 1, static_cast<int64_t>(b.end() - 1 - a.at) / a.step);
+  auto hits = [&](int64_t i) {
+    const int64_t lo = static_cast<int64_t>(a.at - b.at) + i * a.step, hi = lo + a.run;  // from b's start
+    if (hi <= 0 || lo >= (b.rows - 1) * b.step + b.run) return false;
+    if (lo < 0) return true;
+    const int64_t in = lo % b.step;
+    return in < b.run || in + a.run > b.step;
+  };
+  const int64_t period = b.rows > 1 ? b.step / std::gcd(a.step, b.step) : 1;
+  for (int64_t i = first; i <= last && i <= first + period; ++i)
+    if (hits(i)) return true;
+  return false;
+}
+
+// Whether one of the `outputs` shares memory with an input or with another output.
+bool outputs_shared(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Span& in : inputs)
+      if (shares(*o, in)) return true;
+    for (const Span* other = outputs.begin(); other != o; ++other)
+      if (shares(*o, *other)) return true;
+  }
+  return false;
+}
+
 // Exactly one of W / qw, of the expected shape.
 int check_operand(const float* W, const qat_qweight* qw, int64_t N, int64_t K) {
   if ((W == nullptr) == (qw == nullptr)) return QAT_ERR_ARG;
   if (!qw) return aligned16(W) ? QAT_OK : QAT_ERR_ALIGN;
   if (!qw->operand || qw->N != N || qw->K != K) return QAT_ERR_ARG;
   return aligned16(qw->operand) ? QAT_OK : QAT_ERR_ALIGN;
+}
+
+// What get_operand reads.
+Span words_span(const float* W, const qat_qweight* qw, int64_t N, int64_t K) {
+  return W ? Span(W, N * K * 4) : Span(qw->operand, N * K * 2);
 }
 
 // The bf16 operand of a weight: taken from `qw`, or produced from fp32 `W`
@@ -202,6 +254,19 @@ int attn_args(const qat_attn* a, const qat_bf16* Q, const qat_bf16* K, const qat
   return QAT_OK;
 }
 
+// The memory of what both directions are given.
+struct AttnSpans {
+  Span Q, K, V, O, lse, cu_q, cu_k;
+  AttnSpans(const AttnArgs& p, const qat_attn& a, const qat_bf16* q, const qat_bf16* k, const qat_bf16* v)
+      : Q(rows_span(q, p.Tq, p.ldq, width(p.heads, p))),
+        K(rows_span(k, p.Tk, p.ldk, width(p.heads / p.group, p))),
+        V(rows_span(v, p.Tk, p.ldv, width(p.heads / p.group, p))),
+        O(rows_span(static_cast<const qat_bf16*>(p.O), p.Tq, p.ldo, width(p.heads, p))),
+        lse(p.lse, p.heads * p.Tq * 4),
+        cu_q(a.cu_q, (static_cast<int64_t>(a.batch) + 1) * 4),
+        cu_k(a.cu_k, (static_cast<int64_t>(a.batch) + 1) * 4) {}
+  static int64_t width(int heads, const AttnArgs& p) { return static_cast<int64_t>(heads) * p.hd; }
+};
 
 }  // namespace
 }  // namespace qat
@@ -626,8 +691,15 @@ int qat_ce_fwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
   float* tlogit = static_cast<float*>(ws.take(static_cast<size_t>(T) * 4));
   j.parts = ws.take(ce_parts_bytes(T));
   if (!stats || !tlogit || !j.parts) return QAT_ERR_WORKSPACE;
+  int rc = check_operand(W, qw, V, d);
+  if (rc) return rc;
+  const size_t used = ws.used + (W ? operand_bytes(V, d) : 0);
+  if (used > ws_bytes) return QAT_ERR_WORKSPACE;
+  if (outputs_shared({Span(loss, T * 4), Span(lse, T * 4), Span(mean, 8), Span(workspace, used)},
+                     {rows_span(Z, T, ldz, d), Span(targets, T * 8), words_span(W, qw, V, d)}))
+    return QAT_ERR_ARG;
   const __nv_bfloat16* op = nullptr;
-  int rc = get_operand(W, qw, V, d, bits, ws, stream, &op);
+  rc = get_operand(W, qw, V, d, bits, ws, stream, &op);
   if (rc) return rc;
   GemmDesc g;  // logits = Z . Wq^T, as tiles that only the epilogue sees
   g.A = Z; g.lda = ldz;
@@ -693,7 +765,12 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
   // (a smaller workspace than asked for may leave no room for these: the product is then whole)
   const size_t slab_bytes = dZ ? ce_slab_bytes_max(V, d, T, rows) : 0;
   float* slabs = slab_bytes ? static_cast<float*>(ws.take(slab_bytes)) : nullptr;
-  if (dZ == Z) return QAT_ERR_ARG;  // dW reads the rows of Z after their dZ is written
+  // (dW reads the rows of Z after their dZ is written)
+  if (outputs_shared({Span(dZ, T * d * 2), Span(dW, static_cast<int64_t>(V) * d * 4),
+                      Span(workspace, std::min(ws.used, ws_bytes))},
+                     {rows_span(Z, T, ldz, d), Span(targets, T * 8), Span(lse, T * 4), Span(dloss, T * 4),
+                      Span(gscale, 4), words_span(W, qw, V, d)}))
+    return QAT_ERR_ARG;
   const __nv_bfloat16* op = nullptr;
   rc = get_operand(W, qw, V, d, bits, operand_ws, stream, &op);
   if (rc) return rc;
@@ -823,6 +900,10 @@ int qat_rope(const void* X, int64_t ldx, void* Y, int64_t ldy, int32_t dtype, in
   if (T == 0) return QAT_OK;
   if (!aligned16(X) || !aligned16(Y)) return QAT_ERR_ALIGN;
   if (X == Y && ldx != ldy) return QAT_ERR_ARG;
+  const int64_t b = dtype == QAT_DTYPE_BF16 ? 2 : 4;
+  const Span x(X, T, ldx * b, width * b), y(Y, T, ldy * b, width * b);
+  if (outputs_shared({y}, {X == Y ? Span(nullptr, 0) : x, Span(freqs, rotary / 2 * 8), Span(positions, T * 8)}))
+    return QAT_ERR_ARG;
   RopeArgs r{};
   r.X = X;
   r.Y = Y;
@@ -848,7 +929,8 @@ int qat_attn_fwd(const qat_attn* a, const qat_bf16* Q, const qat_bf16* K, const 
   const int rc = attn_args(a, Q, K, V, O, lse, &p);
   if (rc) return rc;
   if (p.Tq == 0 || p.batch == 0 || p.max_q == 0) return QAT_OK;
-  if (O == Q || O == K || O == V) return QAT_ERR_ARG;
+  const AttnSpans m(p, *a, Q, K, V);
+  if (outputs_shared({m.O, m.lse}, {m.Q, m.K, m.V, m.cu_q, m.cu_k})) return QAT_ERR_ARG;
   return launch_attn_fwd(p, stream);
 }
 
@@ -875,10 +957,11 @@ int qat_attn_bwd(const qat_attn* a, const qat_bf16* dO, int64_t lddo, const qat_
   p.delta = static_cast<float*>(ws.take(static_cast<size_t>(p.heads) * p.Tq * 4));
   if (p.Tq > 0 && !p.delta) return QAT_ERR_WORKSPACE;
   // the second kernel reads Q, K, V and dO when dQ is written already
-  for (const qat_bf16* g : {dQ, dK, dV})
-    for (const qat_bf16* in : {Q, K, V, O, dO})
-      if (g && g == in) return QAT_ERR_ARG;
-  if ((dQ && (dQ == dK || dQ == dV)) || (dK && dK == dV)) return QAT_ERR_ARG;
+  const AttnSpans m(p, *a, Q, K, V);
+  if (outputs_shared({rows_span(dQ, p.Tq, p.lddq, wq), rows_span(dK, p.Tk, p.lddk, wk),
+                      rows_span(dV, p.Tk, p.lddv, wk), Span(p.delta, p.Tq > 0 ? p.heads * p.Tq * 4 : 0)},
+                     {m.Q, m.K, m.V, m.O, m.lse, m.cu_q, m.cu_k, rows_span(dO, p.Tq, p.lddo, wq)}))
+    return QAT_ERR_ARG;
   p.dO = dO;
   p.dQ = dQ;
   p.dK = dK;

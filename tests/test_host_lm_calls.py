@@ -35,3 +35,85 @@ def test_ce_bwd_refuses_before_it_quantizes_the_head():
         rows = dict(W=raw["W"], V=V, d=d, Z=raw["Z"], ws=raw["ws"])
         assert call(ldz=(1 << 38) + 8, **rows) == qat.QAT_ERR_SHAPE
     assert qat.launch_count() == before
+
+
+# ------------------------------------------------ memory that arguments share
+
+# More query blocks than a grid holds: such a call is refused after its arguments have been
+# looked at and before anything is launched, so made-up addresses are safe everywhere.
+TOO_LONG = (1 << 31) - 1
+
+
+def runs(at, rows, ld, cols):
+    """Byte ranges of a bf16 row tensor."""
+    return [(at + 2 * ld * i, at + 2 * (ld * i + cols)) for i in range(rows)]
+
+
+def meet(a, b):
+    return any(x0 < y1 and y0 < x1 for x0, x1 in a for y0, y1 in b)
+
+
+def test_overlap_is_found_exactly():
+    """Two row tensors of any starts, strides and lengths, against their byte ranges."""
+    import random
+    rng = random.Random(5)
+    base, before, seen = 0x4000000000, qat.launch_count(), [0, 0]
+    P = [at(0x10000000 * i) for i in range(1, 9)]
+    for n in range(4000):
+        H, KH, hd = rng.choice([(1, 1, 8), (2, 1, 8), (3, 1, 16)])
+        wq, wk = H * hd, KH * hd
+        Tq, Tk = rng.randint(1, 9), rng.randint(1, 9)
+        ldq, ldk = wq + 8 * rng.randint(0, 8), wk + 8 * rng.randint(0, 8)
+        if n % 3 == 0:
+            ldk = ldq if wk <= ldq else ldk
+        o, k = base + 16 * rng.randint(0, 90), base + 16 * rng.randint(0, 90)
+        shared = meet(runs(o, Tq, ldq, wq), runs(k, Tk, ldk, wk))
+        seen[shared] += 1
+        want = qat.QAT_ERR_ARG if shared else None
+        kw = dict(Tq=Tq, Tk=Tk, heads=H, kv_heads=KH, head_dim=hd, batch=1, max_q=TOO_LONG, max_k=TOO_LONG,
+                  cu_q=0x5000, cu_k=0x6000)
+        fwd = attn(Q=P[0], K=at(k), V=P[1], O=at(o), lse=P[2], ldk=ldk, ldo=ldq, **kw)
+        bwd = attn(Q=P[0], K=P[1], V=P[2], O=P[3], lse=P[4], dO=P[5], dQ=at(o), dK=at(k), dV=P[6], lddq=ldq, lddk=ldk,
+                   ws=P[7], **kw)
+        inp = attn(Q=P[0], K=P[1], V=at(k), O=P[3], lse=P[4], dO=P[5], dQ=at(o), dK=P[2], dV=P[6], lddq=ldq, ldv=ldk,
+                   ws=P[7], **kw)
+        for rc in (fwd, bwd, inp):
+            assert rc != qat.QAT_OK and (rc == qat.QAT_ERR_ARG) == shared, (n, rc, shared)
+    assert min(seen) > 500 and qat.launch_count() == before
+
+
+def test_overlapping_views_are_refused():
+    """Not only equal addresses: a view from another offset, statistics in a row tensor's
+    memory, the workspace in an argument's."""
+    before = qat.launch_count()
+    T, V, d = 8, 64, 64
+    A = {n: 0x10000000 * i for i, n in enumerate(("Z", "targets", "loss", "lse", "mean", "ws", "dZ", "dW", "dloss",
+                                                   "gscale", "op"), 1)}
+    sizes = dict(Z=T * d * 2, targets=T * 8, loss=T * 4, lse=T * 4, mean=8, dZ=T * d * 2, dW=V * d * 4, dloss=T * 4,
+                 gscale=4, op=V * d * 2)
+
+    def ce(call, names, **moved):
+        a = {**A, **moved}
+        return call(qw=operand(V, d, a["op"]), V=V, d=d, T=T, **{n: at(a[n]) for n in names})
+
+    fwd, bwd = ("Z", "targets", "loss", "lse", "mean", "ws"), ("Z", "targets", "lse", "dloss", "gscale", "dZ", "dW", "ws")
+    for call, names, outs in ((ce_fwd, fwd, ("loss", "lse", "mean")), (ce_bwd, bwd, ("dZ", "dW"))):
+        for out in outs:
+            for other in names + ("op",):
+                if other == out:
+                    continue
+                end = 16 if other == "ws" else sizes[other] // 16 * 16 - 16
+                assert ce(call, names, **{out: A[other] + max(end, 0)}) == qat.QAT_ERR_ARG, (out, other)
+                if other in sizes and sizes[out] > 16:
+                    back = (sizes[out] - 1) // 16 * 16
+                    assert ce(call, names, **{out: A[other] - back}) == qat.QAT_ERR_ARG, (out, other)
+    assert rope(X=at(0x10000), Y=at(0x10000 + 16), T=4) == qat.QAT_ERR_ARG
+    assert rope(X=at(0x10000), Y=at(0x10000 + 3 * 256), T=4) == qat.QAT_ERR_ARG
+    assert rope(X=at(0x10000), Y=at(0x30000), freqs=at(0x30000 + 512), T=4) == qat.QAT_ERR_ARG
+    assert rope(X=at(0x10000), Y=at(0x30000), pos=at(0x30000 - 24), T=4) == qat.QAT_ERR_ARG
+    q = dict(Q=at(0x100000), K=at(0x200000), V=at(0x300000), O=at(0x400000), lse=at(0x500000))
+    assert attn(**{**q, "lse": at(0x400000 + 64)}) == qat.QAT_ERR_ARG
+    assert attn(**q, dO=at(0x600000), dQ=at(0x700000), dK=at(0x800000), dV=at(0x900000),
+                ws=at(0x500000 + 512)) == qat.QAT_ERR_ARG
+    assert attn(**{**q, "cu_q": 0x400000 + 4}) == qat.QAT_ERR_ARG
+    assert qat.launch_count() == before
