@@ -495,7 +495,7 @@ def _attn(where, Q, K, V, O, lse, heads, kv_heads, head_dim, causal, window, sca
     queries do; without a table the rows are sequences of max_q (max_k) each."""
     bf, wq, wk = torch.bfloat16, heads * head_dim, kv_heads * head_dim
     Tq, Tk = Q.shape[0], K.shape[0]
-    if cu_k is None and not max_k:
+    if cu_k is None and max_k is None:
         cu_k, max_k = cu_q, max_q
     # the C side takes 32 bits, scale 0 for its default, and cuts lengths to max_q and max_k
     if (max_q is None or max_k is None or (scale is not None and not 2.0 ** -126 <= scale < 2.0 ** 127)

@@ -65,3 +65,21 @@ def test_ce_logits_of_minus_infinity_weigh_nothing(T):
     assert torch.equal(loss, lse)
     W[:, 0] = -10.0
     assert bool((ce_loss(Z, targets, W)[1] == -math.inf).all())
+
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_attention_over_no_keys(packed):
+    """max_k = 0 and no table of keys: every query sees nothing, forward and backward."""
+    H, KH, hd, n = 2, 1, 64, 8
+    rows = lambda m, heads: torch.randn(m, heads * hd, device="cuda").to(BF)
+    q, k, v, do = rows(n, H), rows(0, KH), rows(0, KH), rows(n, H)
+    o, dq, lse = torch.full_like(q, 7.0), torch.full_like(q, 7.0), torch.zeros(H, n, device="cuda")
+    kw = dict(max_q=4, max_k=0)
+    if packed:
+        kw["cu_q"] = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
+    ws = torch.empty(qat.workspace_size(qat.QAT_OP_ATTN_BWD, H, hd, n, False), dtype=torch.uint8, device="cuda")
+    qat.qat_attn_fwd(q, k, v, o, lse, H, KH, hd, **kw)
+    qat.qat_attn_bwd(do, q, k, v, o, lse, dq, torch.empty_like(k), torch.empty_like(v), H, KH, hd, workspace=ws, **kw)
+    torch.cuda.synchronize()
+    assert qat.device_error() == 0
+    assert not o.any() and not dq.any() and bool((lse == -math.inf).all())

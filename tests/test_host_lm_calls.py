@@ -117,3 +117,25 @@ def test_overlapping_views_are_refused():
                 ws=at(0x500000 + 512)) == qat.QAT_ERR_ARG
     assert attn(**{**q, "cu_q": 0x400000 + 4}) == qat.QAT_ERR_ARG
     assert qat.launch_count() == before
+
+
+# ------------------------------------------------------------------ binding
+
+def descriptor(monkeypatch, Tq, Tk, **kw):
+    monkeypatch.setattr(qat, "_need", lambda *a: None)
+    rows = lambda n, w: torch.zeros(n, w, dtype=torch.bfloat16)
+    q, k = rows(Tq, 128), rows(Tk, 64)
+    d = dict(cu_q=None, cu_k=None, max_q=None, max_k=None)
+    return qat._attn("call", q, k, k, q, torch.zeros(2, Tq), 2, 1, 64, True, 0, None, **{**d, **kw})
+
+
+def test_no_keys_is_not_keys_as_queries(monkeypatch):
+    """max_k = 0 says that no sequence has a key; only max_k left out says that the keys
+    lie as the queries do."""
+    cu = torch.tensor([0, 3, 7], dtype=torch.int32)
+    a = descriptor(monkeypatch, 7, 0, cu_q=cu, max_q=4, max_k=0)
+    assert (a.batch, a.Tq, a.Tk, a.max_q, a.max_k, a.cu_k) == (2, 7, 0, 4, 0, None)
+    a = descriptor(monkeypatch, 8, 0, max_q=4, max_k=0)
+    assert (a.batch, a.max_k, a.cu_k) == (2, 0, None)
+    a = descriptor(monkeypatch, 7, 7, cu_q=cu, max_q=4)
+    assert (a.batch, a.max_k) == (2, 4) and a.cu_k == a.cu_q
