@@ -412,6 +412,16 @@ def _whole(where, *tensors):
             raise QatError(QAT_ERR_ARG, where)
 
 
+def _scratch(where, ws):
+    """Address and bytes of a workspace.  One on another device, or one whose elements do
+    not lie behind one another (a broadcast one), holds less than the count says: refused."""
+    if ws is None:
+        return None, 0
+    _whole(where, ws)
+    _need(where, (ws, ws.dtype, 0))
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _head(where, W, qw):
     if (W is None) == (qw is None):
         raise QatError(QAT_ERR_ARG, where)
@@ -435,7 +445,7 @@ def qat_ce_fwd(Z, targets, loss, lse, bits, W=None, qw=None, mean=None, workspac
     _need(f, (Z, torch.bfloat16, 0), (targets, torch.int64, T), (loss, f32, T), (lse, f32, T),
           (mean, f32, 2))
     _whole(f, targets, loss, lse, mean)
-    ws, wsb = _ws(workspace)
+    ws, wsb = _scratch(f, workspace)
     _check(lib().qat_ce_fwd(_p(W), _qref(qw), V, d, bits, _p(Z), ldz, T, _p(targets), _p(loss),
                             _p(lse), _p(mean), ws, wsb, _stream(stream)), f)
 
@@ -451,7 +461,7 @@ def qat_ce_bwd(Z, targets, lse, bits, W=None, qw=None, dloss=None, gscale=None, 
     _need(f, (Z, torch.bfloat16, 0), (targets, torch.int64, T), (lse, f32, T), (dloss, f32, T),
           (gscale, f32, 1), (dZ, torch.bfloat16, T * d), (dW, f32, V * d))
     _whole(f, targets, lse, dloss, dZ, dW)
-    ws, wsb = _ws(workspace)
+    ws, wsb = _scratch(f, workspace)
     _check(lib().qat_ce_bwd(_p(W), _qref(qw), V, d, bits, _p(Z), ldz, T, _p(targets), _p(lse),
                             _p(dloss), _p(gscale), _p(dZ), _p(dW), int(bool(accumulate_dW)), ws,
                             wsb, _stream(stream)), f)
@@ -541,7 +551,7 @@ def qat_attn_bwd(dO, Q, K, V, O, lse, dQ, dK, dV, heads, kv_heads, head_dim, cau
     a = _attn(f, Q, K, V, O, lse, heads, kv_heads, head_dim, causal, window, scale, cu_q, cu_k,
               max_q, max_k)
     _need(f, (dO, bf, 0), (dQ, bf, 0), (dK, bf, 0), (dV, bf, 0))
-    ws, wsb = _ws(workspace)
+    ws, wsb = _scratch(f, workspace)
     _check(lib().qat_attn_bwd(ctypes.byref(a), _p(dO), _rows(f, dO, wq, a.Tq), _p(Q), _p(K), _p(V),
                               _p(O), _p(lse), _p(dQ), _rows(f, dQ, wq, a.Tq), _p(dK),
                               _rows(f, dK, wk, a.Tk), _p(dV), _rows(f, dV, wk, a.Tk), ws, wsb,

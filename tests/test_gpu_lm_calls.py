@@ -83,3 +83,23 @@ def test_attention_over_no_keys(packed):
     torch.cuda.synchronize()
     assert qat.device_error() == 0
     assert not o.any() and not dq.any() and bool((lse == -math.inf).all())
+
+
+def test_workspaces_of_another_device_or_with_gaps_are_refused():
+    T, V, d, H, hd = 8, 64, 64, 2, 64
+    Z, t = torch.zeros(T, d, dtype=BF, device="cuda"), torch.zeros(T, dtype=torch.int64, device="cuda")
+    q = qat.QWeight(torch.zeros(V, d, dtype=BF, device="cuda"), None, None, 8)
+    loss, lse = torch.zeros(T, device="cuda"), torch.zeros(T, device="cuda")
+    rows = [torch.zeros(T, H * hd, dtype=BF, device="cuda") for _ in range(8)]
+    stats = torch.zeros(H, T, device="cuda")
+    n = 1 << 20
+    before = qat.launch_count()
+    for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(n),
+               torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        for call in (lambda: qat.qat_ce_fwd(Z, t, loss, lse, 8, qw=q, workspace=ws),
+                     lambda: qat.qat_ce_bwd(Z, t, lse, 8, qw=q, dZ=torch.empty_like(Z), workspace=ws),
+                     lambda: qat.qat_attn_bwd(*rows[:5], stats, *rows[5:], H, H, hd, max_q=T, workspace=ws)):
+            with pytest.raises(qat.QatError) as e:
+                call()
+            assert e.value.code == qat.QAT_ERR_ARG
+    assert qat.launch_count() == before

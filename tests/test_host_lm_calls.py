@@ -139,3 +139,21 @@ def test_no_keys_is_not_keys_as_queries(monkeypatch):
     assert (a.batch, a.max_k, a.cu_k) == (2, 0, None)
     a = descriptor(monkeypatch, 7, 7, cu_q=cu, max_q=4)
     assert (a.batch, a.max_k) == (2, 4) and a.cu_k == a.cu_q
+
+
+def test_workspaces_that_hold_less_than_they_count_are_refused(monkeypatch):
+    """The C side takes an address and a size: broadcast or gapped workspaces, and those of
+    another device, never reach it."""
+    place = [0]  # of the current device; host tensors are on none (-1)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: place[0])
+    whole = torch.zeros(64, dtype=torch.uint8)
+    for ws in (whole[:1].expand(1 << 20), whole[::2], whole):
+        with pytest.raises(qat.QatError) as e:
+            qat._scratch("call", ws)
+        assert e.value.code == qat.QAT_ERR_ARG
+    place[0] = -1
+    assert qat._scratch("call", whole[16:]) == (whole.data_ptr() + 16, 48)
+    assert qat._scratch("call", None) == (None, 0)
+    for ws in (whole[:1].expand(1 << 20), whole[::2]):
+        with pytest.raises(qat.QatError):
+            qat._scratch("call", ws)
