@@ -474,6 +474,8 @@ def rope_freqs(rotary, base=10000.0, scaling="none", factor=1.0, trained_len=0, 
     "linear", "ntk" or "yarn" (contexts `factor` times the trained length)."""
     if scaling not in _ROPE_SCALINGS or rotary < 2 or rotary % 2:
         raise QatError(QAT_ERR_ARG, "rope_freqs")
+    if rotary > QAT_ROPE_MAX_DIMS:  # (before its table is made, and before 32 bits wrap it)
+        raise QatError(QAT_ERR_SHAPE, "rope_freqs")
     f, m = (ctypes.c_double * (rotary // 2))(), ctypes.c_double(1.0)
     _check(lib().qat_rope_freqs(rotary, base, _ROPE_SCALINGS[scaling], factor, int(trained_len),
                                 beta_fast, beta_slow, ctypes.cast(f, ctypes.c_void_p),

@@ -157,3 +157,11 @@ def test_workspaces_that_hold_less_than_they_count_are_refused(monkeypatch):
     for ws in (whole[:1].expand(1 << 20), whole[::2]):
         with pytest.raises(qat.QatError):
             qat._scratch("call", ws)
+
+
+def test_rope_freqs_of_more_dims_than_32_bits_hold():
+    """Refused before the table is made (of 2^31 pairs) and not taken as 8 dims."""
+    for rotary in ((1 << 32) + 8, 1 << 40, qat.QAT_ROPE_MAX_DIMS + 2):
+        with pytest.raises(qat.QatError) as e:
+            qat.rope_freqs(rotary, device="cpu")
+        assert e.value.code == qat.QAT_ERR_SHAPE
