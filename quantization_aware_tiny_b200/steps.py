@@ -329,7 +329,8 @@ class RecurrentCore:
 
     def flops(self, T, R):
         """Of the linears (attention's depend on the sequences)."""
-        return 2.0 * T * self.d * (self.nqkv + self.d + 2 * self.H) * R
+        o = self.d if self.attention is None else self.W[1].shape[1]
+        return 2.0 * T * self.d * (self.nqkv + o + 2 * self.H) * R
 
     def flops_bwd(self, T, R):
         """Contractions of backward()'s linears: per application the MLP's four
