@@ -263,10 +263,13 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
  * range of a wider row, such as the query and key columns of a Q|K|V
  * projection.  Y may be X itself (same stride); otherwise they share
  * no elements (columns of one wider row are fine).  head_dim a multiple of 8; rotary even, at most head_dim and
- * QAT_ROPE_MAX_DIMS.  positions [T] int64 (any value), or NULL: row t is at
- * t mod seq_len, or at t with seq_len = 0.  freqs [rotary / 2] fp64, turns per
- * position: angles are reduced to a part of a turn in fp64, so far positions
- * keep fp32's accuracy.  The rotation is computed in fp32 and rounded once.
+ * QAT_ROPE_MAX_DIMS.  positions [T] int64, or NULL: row t is at t mod seq_len,
+ * or at t with seq_len = 0.  freqs [rotary / 2] fp64, turns per position: the
+ * whole turns are taken off the exact product, so the angle of the given freqs
+ * keeps fp32's accuracy at every position to +-2^53 (farther ones are themselves
+ * rounded to 53 bits).  What a frequency lost when it was rounded to fp64 grows
+ * with the position: up to 2 pi |n| freqs[i] 2^-53 radians, 2.4e-7 at 2^31 and one
+ * radian a position.  The rotation is computed in fp32 and rounded once.
  * ------------------------------------------------------------------------- */
 #define QAT_ROPE_MAX_DIMS 1024
 int qat_rope(const void* X, int64_t ldx, void* Y, int64_t ldy, int32_t dtype, int64_t T,

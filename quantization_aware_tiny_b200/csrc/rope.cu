@@ -4,9 +4,12 @@
 // the rest of the head is copied.  Bound by reading and writing the rows once.
 //
 // The angle is the same for all heads of a token, so a block computes the
-// sines of its tokens once into shared memory (position * turns in 64 bits,
-// only the fraction of a turn kept: exact to 2^-53 of the position, where an
-// fp32 product is a whole turn off at two million) and then streams the rows.
+// sines of its tokens once into shared memory and then streams the rows.  Only
+// the fraction of a turn is kept: the whole turns, from the product position *
+// freqs in 64 bits, are taken off its exact value by a multiply-add, so what is
+// left is off by 2^-54 at any position (one radian a position: the rounded
+// product's own fraction is 1e-4 radians off at 2^40, an fp32 product's a whole
+// turn at two million).
 #include <algorithm>
 #include <type_traits>
 
@@ -91,9 +94,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs r, int to
   for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
     const int t = i / pairs, k = i - t * pairs;
     const int64_t pos = r.positions ? r.positions[t0 + t] : (r.seq_len > 0 ? (t0 + t) % r.seq_len : t0 + t);
-    const double turns = static_cast<double>(pos) * r.freqs[k];
+    const double n = static_cast<double>(pos), freq = r.freqs[k];
     float s, c;
-    sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &c);
+    sincospif(2.0f * static_cast<float>(fma(n, freq, -rint(n * freq))), &s, &c);
     table[t * stride + k] = make_float2(c * r.scale, (r.inverse ? -s : s) * r.scale);
   }
   __syncthreads();

@@ -103,3 +103,33 @@ def test_workspaces_of_another_device_or_with_gaps_are_refused():
                 call()
             assert e.value.code == qat.QAT_ERR_ARG
     assert qat.launch_count() == before
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_far_positions_against_exact_products(interleaved):
+    """To positions of +-2^53: the fraction of a turn of position * freqs in whole numbers,
+    where a product rounded to 64 bits is off by 1e-4 radians at 2^40 and by one at 2^53."""
+    from fractions import Fraction
+    from test_gpu_rope import PAIR
+    heads, hd, rot = 2, 32, 24
+    freqs, m = qat.rope_freqs(rot, scaling="yarn", factor=4.0, trained_len=1024)
+    places = [s * (2 ** e + k) for e in (31, 36, 40, 46, 52) for k in (0, 12345, -77) for s in (1, -1)]
+    places += [2 ** 53, -(2 ** 53)]
+    x = torch.randn(len(places), heads * hd, generator=torch.Generator().manual_seed(2))
+    y = torch.empty(len(places), heads * hd, device="cuda")
+    qat.qat_rope(x.cuda(), y, heads, hd, freqs, positions=torch.tensor(places, device="cuda"), scale=m,
+                 interleaved=interleaved)
+    torch.cuda.synchronize()
+    want = f64(x).reshape(-1, heads, hd).clone()
+    tol = torch.zeros_like(want)
+    i = torch.arange(rot // 2)
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
+    turn = torch.tensor([[float(Fraction(n) * Fraction(f) % 1) for f in freqs.tolist()] for n in places],
+                        dtype=torch.float64) * 2 * math.pi
+    c, s = m * turn.cos()[:, None], m * turn.sin()[:, None]
+    u, v = want[..., a].clone(), want[..., b].clone()
+    want[..., a], want[..., b] = u * c - v * s, u * s + v * c
+    tol[..., a] = tol[..., b] = PAIR * m * (u.abs() + v.abs())
+    tol += 2.0 ** -24 * want.abs()
+    err = (f64(y).reshape(want.shape) - want).abs()
+    assert bool((err <= tol).all()), float((err - tol).max())
