@@ -312,7 +312,8 @@ int qat_rope_freqs(int32_t rotary, double base, int32_t scaling, double factor,
  * 8 up to 128.  Products and sums are fp32; P and dS are rounded to bf16 as
  * operands of the second products.  The same inputs give the same bits.  Outputs
  * share no elements with inputs or with one another (interleaved columns of one
- * wider row are fine).  max_q, and for the backward max_k, up to 65,535 * 128.
+ * wider row are fine).  max_q, and for the backward max_k, up to 65,535 * 128;
+ * the smaller of max_k and Tk up to 2^26 where max_q is over 128.
  * ------------------------------------------------------------------------- */
 #define QAT_ATTN_MAX_HEAD_DIM 128
 typedef struct qat_attn {

@@ -212,6 +212,13 @@ size_t ce_slab_bytes_max(int64_t V, int64_t d, int64_t T, int64_t rows) {
 }
 
 // ---- attention
+// Longest sequence of keys under more than 128 queries.  The second tile of a piece of
+// work may have no queries, and its warps then wait for the next piece while the first
+// tile walks all keys: about 2 us a block of 128, 1.1 s of the 2 s after which a device-side
+// wait gives up.  (The backward's grids end at 65,535 * 128 keys; up to 128 queries both
+// tiles walk.)
+constexpr int64_t kAttnMaxKeys = 1ll << 26;
+
 // The checks that both directions share; fills the kernels' arguments.
 int attn_args(const qat_attn* a, const qat_bf16* Q, const qat_bf16* K, const qat_bf16* V,
               const qat_bf16* O, const float* lse, AttnArgs* out) {
@@ -929,6 +936,7 @@ int qat_attn_fwd(const qat_attn* a, const qat_bf16* Q, const qat_bf16* K, const 
   const int rc = attn_args(a, Q, K, V, O, lse, &p);
   if (rc) return rc;
   if (p.Tq == 0 || p.batch == 0 || p.max_q == 0) return QAT_OK;
+  if (p.max_q > 128 && std::min<int64_t>(p.max_k, p.Tk) > kAttnMaxKeys) return QAT_ERR_SHAPE;
   const AttnSpans m(p, *a, Q, K, V);
   if (outputs_shared({m.O, m.lse}, {m.Q, m.K, m.V, m.cu_q, m.cu_k})) return QAT_ERR_ARG;
   return launch_attn_fwd(p, stream);

@@ -165,3 +165,16 @@ def test_rope_freqs_of_more_dims_than_32_bits_hold():
         with pytest.raises(qat.QatError) as e:
             qat.rope_freqs(rotary, device="cpu")
         assert e.value.code == qat.QAT_ERR_SHAPE
+
+
+def test_walks_that_would_outlast_the_bounded_waits_are_refused():
+    """More than 2^26 keys under more than 128 queries: one tile of a piece would wait for the
+    other's whole walk."""
+    P = [at(0x10000000 * i) for i in range(1, 6)]
+    keys = (1 << 26) + 1
+    long = dict(Q=P[0], K=at(0x1000000000), V=at(0x9000000000), O=P[3], lse=P[4], heads=1, kv_heads=1, head_dim=8,
+                max_q=129, Tq=129, max_k=keys, Tk=keys)
+    before = qat.launch_count()
+    assert attn(**long) == qat.QAT_ERR_SHAPE
+    assert attn(**{**long, "cu_k": 0x5000, "max_k": TOO_LONG}) == qat.QAT_ERR_SHAPE
+    assert qat.launch_count() == before
