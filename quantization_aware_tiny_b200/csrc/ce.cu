@@ -1,7 +1,8 @@
 // Reductions of the softmax cross entropy.  The logits themselves only ever
 // exist as accumulator tiles of the GEMM (its EPI_CE_STATS and EPI_CE_GRAD
 // epilogues); what reaches global memory is one (max, sum) pair per token and
-// 128 columns, joined here.
+// 128 columns (64 where the narrow tile is chosen: two warps share a tile's
+// columns), joined here.
 #include <algorithm>
 
 #include "lm_ops.cuh"

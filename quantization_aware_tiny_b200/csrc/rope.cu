@@ -50,9 +50,10 @@ __device__ __forceinline__ void store(T* p, const Pack<T>& r) {
   *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(r.v);
 }
 
-// n / d for 0 <= n < 2^31 by a multiply-high and a shift (the round-up method: m =
-// floor(2^32 (2^l - d) / d) + 1 with 2^(l-1) < d <= 2^l): two divisions a pack were
-// most of the kernel's instructions.
+// n / d for 0 <= n < 2^31 by a multiply-high and a shift (Granlund and Montgomery,
+// "Division by invariant integers using multiplication", 1994: m = floor(2^32 (2^l - d)
+// / d) + 1 with 2^(l-1) < d <= 2^l): two divisions a pack were most of the kernel's
+// instructions.
 struct FastDiv {
   uint32_t m, l, d;
   explicit FastDiv(uint32_t div) : d(div) {

@@ -417,9 +417,9 @@ def _scratch(where, ws):
     not lie behind one another (a broadcast one), holds less than the count says: refused."""
     if ws is None:
         return None, 0
-    _whole(where, ws)
-    _need(where, (ws, ws.dtype, 0))
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    if not ws.is_contiguous() or ws.get_device() != torch._C._cuda_getDevice():
+        raise QatError(QAT_ERR_ARG, where)
+    return ws.data_ptr(), ws.nbytes
 
 
 def _head(where, W, qw):
