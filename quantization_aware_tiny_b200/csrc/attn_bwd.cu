@@ -15,12 +15,16 @@
 // 128 x 128 block in dq and 3,300 in dkv at head size 64, where the products take
 // 768 and 1,024 and the exponentials 1,024): tensor memory loads and stores, and
 // barriers, each some 150 to 400 cycles with 16 warps at them.  4 sequences of 4,096
-// tokens, 8 heads of 64 over 4: dq 164 us, dkv 200 us together with it 334 us
-// (515 TFLOP/s of the 5 products that have to be); 8,192 tokens of 128, 8 over 2:
-// 690 us.  Exponentials partly on the multiply-add units, two issuing warps, and P
-// and dS handed over together gained nothing or lost.
+// tokens, 8 heads of 64 over 4: dq 150 us and dkv 190 us (334 to 340 us together,
+// 505 to 515 TFLOP/s of the 5 products that have to be); 8,192 tokens of 128, 8 over
+// 2: 179 and 509 us, 690 together (a key tile's block walks all 4 heads of its group).  Exponentials
+// partly on the multiply-add units, two issuing warps, and P and dS handed over together
+// gained nothing or lost.
 //
-// P and dS are rounded to bf16 for the second products.  They go back to tensor
+// P and dS are rounded to bf16 for the second products, as P is in the forward: each
+// off by at most 2^-8 of itself, which leaves dQ, dK and dV 2.5e-3 off in the 2-norm
+// where their own rounding alone gives 1.7e-3; second halves would be three products
+// more.  delta, lse and all sums are fp32.  They go back to tensor
 // memory and are read from there as operand A.  Both kernels form P as soon as S
 // is there and dS once dP is, so that the products of the next block (and the
 // sums of this one) run below the exponentials; four math warpgroups share a
@@ -46,6 +50,7 @@ struct Cfg {
   static constexpr int MC = BT / GROUPS;            // columns of a block per thread
   static constexpr int THREADS = 128 * (1 + GROUPS);
   // registers per thread: 96 at launch (65,536 / 640), 56 + 4 * 104 <= 5 * 96 after the split
+  // (dkv keeps 28 to 40 bytes a thread in local memory, dq none)
   static constexpr int REGS_ISSUE = 56, REGS_MATH = 104;
   static constexpr int TILE = tile_bytes(BT, NC);
   static constexpr int ST = NC == 1 ? 4 : 2;        // stages of either ring

@@ -174,7 +174,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 // Gradient of one 32-column chunk, g = (softmax - [target]) * scale, staged as
 // bf16(g) in buf0 and, with keep_lo, bf16(g - bf16(g)) in buf1 (32 rows x 64 B,
-// swizzled as stage_chunk does), two columns an instruction.
+// swizzled as stage_chunk does), two columns an instruction.  The tensor core takes
+// bf16: dZ = bf16(g . W) reads the first half, each element off by at most 2^-8 of
+// itself, which over a row's words comes to less than dZ's own rounding once the
+// target's element (the one that does not average out) is mended with its remainder;
+// dW is fp32 and reads both halves, which leave 2^-16 of g.
 __device__ __forceinline__ void stage_grad_chunk(const KArgs& p, const uint32_t (&acc)[32], int col0,
                                                  int row, const CeRow& c, uint32_t buf0, uint32_t buf1,
                                                  bool keep_lo, int lane) {
