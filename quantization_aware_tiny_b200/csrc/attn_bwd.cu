@@ -15,9 +15,9 @@
 // 128 x 128 block in dq and 3,300 in dkv at head size 64, where the products take
 // 768 and 1,024 and the exponentials 1,024): tensor memory loads and stores, and
 // barriers, each some 150 to 400 cycles with 16 warps at them.  4 sequences of 4,096
-// tokens, 8 heads of 64 over 4: dq 150 us and dkv 190 us (334 to 340 us together,
-// 505 to 515 TFLOP/s of the 5 products that have to be); 8,192 tokens of 128, 8 over
-// 2: 179 and 509 us, 690 together (a key tile's block walks all 4 heads of its group).  Exponentials
+// tokens, 8 heads of 64 over 4: dq 154 us and dkv 190 us (344 us together, 500 TFLOP/s
+// of the 5 products that have to be); 8,192 tokens of 128, 8 over 2: 182 and 512 us,
+// 695 together (a key tile's block walks all 4 heads of its group).  Exponentials
 // partly on the multiply-add units, two issuing warps, and P and dS handed over together
 // gained nothing or lost.
 //
@@ -54,7 +54,9 @@ struct Cfg {
   static constexpr int REGS_ISSUE = 56, REGS_MATH = 104;
   static constexpr int TILE = tile_bytes(BT, NC);
   static constexpr int ST = NC == 1 ? 4 : 2;        // stages of either ring
-  static constexpr int ROWS_BYTES = 4 * GROUPS * 2 * MC * 4;  // dkv: lse and delta, per warp
+  // dkv: lse and delta, per warp; dq: delta of the rows, and its parts per warpgroup
+  static constexpr int ROWS_BYTES = 4 * GROUPS * 2 * MC * 4;
+  static_assert((1 + GROUPS) * BT * 4 <= ROWS_BYTES, "dq's rows");
   static constexpr int OUT_BYTES = 4 * GROUPS * 1024;  // the gradient rows' way out, per warp
   static constexpr int SMEM = (2 + 2 * ST) * TILE + ROWS_BYTES + OUT_BYTES + 1024 + 512;
   static constexpr int COLS = 64 * NC;              // tensor-memory columns of an accumulator
@@ -67,7 +69,7 @@ struct Smem {
   uint8_t *fix_a, *fix_b, *ring_a, *ring_b, *out;
   float* rows;
   uint64_t *fix_full, *fix_empty, *a_full, *a_empty, *b_full, *b_empty;
-  uint64_t *s_full, *dp_full, *s_read, *p_full, *p_free, *ds_full, *acc_full, *mma_done;
+  uint64_t *s_full, *dp_full, *s_read, *p_full, *p_free, *ds_full, *acc_full, *delta_full, *mma_done;
   uint32_t* tmem_slot;
   volatile int* abort_flag;
 
@@ -91,10 +93,11 @@ struct Smem {
     p_free = p_full + 1;
     ds_full = p_free + 1;
     acc_full = ds_full + 1;
-    mma_done = acc_full + 1;
+    delta_full = acc_full + 1;
+    mma_done = delta_full + 1;
     tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 5);
     abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 + 4 * C::ST + 12) * 8 + 8 <= 512 - 32, "barrier block overflow");
+    static_assert((2 + 4 * C::ST + 13) * 8 + 8 <= 512 - 32, "barrier block overflow");
   }
   __device__ WorkQueue queue() const {
     return WorkQueue{smem_u32(fix_full) + 512 - 32, mma_done + 1, mma_done + 3};
@@ -116,6 +119,7 @@ struct Smem {
     mbar_init(p_free, 1);
     mbar_init(ds_full, 4 * C::GROUPS);
     mbar_init(acc_full, 1);
+    mbar_init(delta_full, 4 * C::GROUPS);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -195,13 +199,29 @@ __device__ __forceinline__ void produce(const Smem<NC>& m, const AttnArgs& p, Wo
 
 // ------------------------------------------------------------------------ dQ
 
+// delta = rowsum(dO * O) comes from the O that was rounded to bf16, and dP - delta
+// takes two near numbers apart where a row's softmax rests on few keys: with two keys
+// dQ and dK were 0.004 to 0.02 off (and anything where one of the two has nearly all the
+// weight), where their roundings leave 0.0024.  By its definition delta is sum(P * dP):
+// sum(P * (dP - delta)) is what it lacks.  A row whose keys lie in one block gets it
+// before its dS is formed (all rows of few keys, but for small windows: those tiles are
+// walked twice, the first time for the sum alone); the others take delta as it came,
+// which costs nothing at scores of unit spread (0.0024) and up to 0.0035 at four times
+// that.  dK always gets the mended delta: the sum goes along with dS.  The sums take 3 %
+// of this kernel (150 -> 154 us at 4 x 4,096 tokens of 8 heads of 64); tiles walked twice
+// are a kernel of their own, since the branch around the products that a common one needs
+// took 9 % more.  At windows past 16 keys dQ is 0.0025 off as it is.
+constexpr int kFewKeys = 16;
+
 // A CTA owns 128 queries of a head.  Tensor memory: S, dP (128 columns each), dS
 // (bf16, 64), dQ.  Issue order: S(n + 1) once S(n) is read; then, once dS(n) is
 // written, dQ += dS(n) K(n) and dP(n + 1) -- whose arrival thus also says that
 // dS(n) has been read.
+template <bool TWICE>
 struct DqPiece {
   Seq sq;
-  int head, kv_head, i0, j0, steps;  // queries from i0 on, key blocks j0 .. j0 + steps - 1
+  int head, kv_head, i0, j0, blocks;  // queries from i0 on, key blocks j0 .. j0 + blocks - 1
+  int steps;                          // blocks walked, all times taken together
   bool live;
 
   __device__ DqPiece(const AttnArgs& p, const Work& w) {
@@ -212,16 +232,20 @@ struct DqPiece {
     live = i0 < sq.nq;
     int j1;
     key_blocks<BT, BT>(p, sq, i0, j0, j1);
-    steps = live ? j1 - j0 : 0;
+    blocks = live ? j1 - j0 : 0;
+    steps = TWICE && blocks > 1 ? 2 * blocks : blocks;
   }
+  __device__ int first() const { return TWICE ? steps - blocks : 0; }  // steps taken for delta alone
+  __device__ int key0(int n) const { return (j0 + (n < first() ? n : n - first())) * BT; }
 };
 
-template <int NC>
+template <int NC, bool TWICE>
 __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     attn_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const AttnArgs p) {
   using C = Cfg<NC>;
+  using PieceT = DqPiece<TWICE>;
   constexpr int ST = C::ST;
   constexpr uint32_t T_DP = BT, T_DS = 2 * BT, T_DQ = 2 * BT + BT / 2;
   static_assert(T_DQ + C::COLS <= 512, "tensor memory");
@@ -251,15 +275,15 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
   if (warp < 4) {
     set_regs_dec<C::REGS_ISSUE>();
     if (warp == 0) {
-      produce<NC, DqPiece>(
+      produce<NC, PieceT>(
           m, p, work, lane,
-          [&](const DqPiece& x) {
+          [&](const PieceT& x) {
             const int row = static_cast<int>(x.sq.q0) + x.i0;
             load_tile<NC>(&tmQ, m.fix_full, m.fix_a, x.head, row);
             load_tile<NC>(&tmdO, m.fix_full, m.fix_b, x.head, row);
           },
-          [&](const DqPiece& x, int n, bool second, uint64_t* bar, uint8_t* dst) {
-            load_tile<NC>(second ? &tmV : &tmK, bar, dst, x.kv_head, static_cast<int>(x.sq.k0) + (x.j0 + n) * BT);
+          [&](const PieceT& x, int n, bool second, uint64_t* bar, uint8_t* dst) {
+            load_tile<NC>(second ? &tmV : &tmK, bar, dst, x.kv_head, static_cast<int>(x.sq.k0) + x.key0(n));
           });
     } else if (warp == 1) {
       // ------------------------------------------------ MMA issuer
@@ -274,13 +298,13 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       bool ok = true;
       int base = 0, loads = 0;  // blocks and fixed tiles of the pieces before
       for (int pieces = 0;; ++pieces) {
-        const DqPiece x(p, work);
+        const PieceT x(p, work);
         // X = fixed streamed^T of block n
         auto scores = [&](int n, uint64_t* full, uint8_t* ring, uint64_t b, uint64_t fix, uint32_t t, uint64_t* done) {
           const int g = base + n, st = g % ST;
           ok = ok && warp_wait(&full[st], (g / ST) & 1, m.abort_flag, p.err);
           if (!ok) return;
-          const int rows = x.sq.nk - (x.j0 + n) * BT;
+          const int rows = x.sq.nk - x.key0(n);
           if (rows < BT) clear_rows<NC>(ring + st * C::TILE, BT, rows, lane);
           tc_fence_after();
           product<NC, BT>(tmem + t, fix, b + st * STAGE, id_s, ks, issue);
@@ -304,9 +328,11 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             const uint64_t k = rows_a + g % ST * STAGE;
+            if (!TWICE || n >= x.first()) {
 #pragma unroll
-            for (int kk = 0; kk < BT / 16; ++kk)
-              mma_ts(tmem + T_DQ, tmem + T_DS + kk * 8, k + rows_step(kk), id_q, (kk > 0) | (n > 0), issue);
+              for (int kk = 0; kk < BT / 16; ++kk)
+                mma_ts(tmem + T_DQ, tmem + T_DS + kk * 8, k + rows_step(kk), id_q, (kk > 0) | (n > x.first()), issue);
+            }
             mma_commit(&m.a_empty[g % ST], issue);
             if (more) {
               scores(n + 1, m.b_full, m.ring_b, ring_b, fix_b, T_DP, m.dp_full);
@@ -333,7 +359,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
     bool ok = true;
     int base = 0, accs = 0;  // blocks of the pieces before, and pieces that had any
     for (int pieces = 0;; ++pieces) {
-      const DqPiece x(p, work);
+      const PieceT x(p, work);
       const int i = x.i0 + quarter * 32 + lane;
       const int64_t at = x.sq.q0 + i;
       int lo, hi;
@@ -376,7 +402,8 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
           const int r = r0 + 2 * k;
           if ((lane & 15) == 0) {
             m.rows[r] = sum;
-            if (x.i0 + r < x.sq.nq) p.delta[x.head * p.Tq + x.sq.q0 + x.i0 + r] = sum;  // for the other kernel
+            // for the other kernel (rows that see no key; the others' is mended first)
+            if (x.steps == 0 && x.i0 + r < x.sq.nq) p.delta[x.head * p.Tq + x.sq.q0 + x.i0 + r] = sum;
           }
         }
         __syncwarp();
@@ -384,7 +411,21 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
       }
       ok = warp_wait(m.p_full, pieces & 1, m.abort_flag, p.err);
       const float delta = m.rows[quarter * 32 + lane];
-      const float2 cc = make_float2(c2, c2), nl = make_float2(-lse2, -lse2), nd = make_float2(-delta, -delta);
+      const float2 cc = make_float2(c2, c2), nl = make_float2(-lse2, -lse2);
+      float2 nd = make_float2(-delta, -delta), lacks = make_float2(0.0f, 0.0f);
+      // -delta with what it lacks: the warpgroups' shares of a row meet in shared memory
+      // (read before any warp leaves this piece's p_full behind again)
+      auto settle = [&]() {
+        float* part = m.rows + BT + quarter * 32 + lane;
+        part[w * BT] = lacks.x + lacks.y;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(m.delta_full);
+        ok = warp_wait(m.delta_full, accs & 1, m.abort_flag, p.err);
+        const float d = delta + ((part[0] + part[BT]) + (part[2 * BT] + part[3 * BT]));
+        if (ok && w == 0 && i < x.sq.nq) p.delta[x.head * p.Tq + at] = d;  // for the other kernel
+        nd = make_float2(-d, -d);
+      };
+      const bool open = x.steps > 1 && x.first() == 0;  // dS is formed before delta is mended
       for (int n = 0; ok && n < x.steps; ++n) {
         if (!warp_wait(m.s_full, (base + n) & 1, m.abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
@@ -394,7 +435,7 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(m.s_read);
-        const int key0 = (x.j0 + n) * BT;
+        const int key0 = x.key0(n);
         // (a query of a single key has no gradient: dS is 0, where dP and delta differ by roundings)
         if (key0 < full0 || key0 + BT > full1) mask_scores(s, lo - key0 - w * 32, hi - lo == 1 ? 0 : hi - lo);
         float2 pr[16];
@@ -407,19 +448,35 @@ __global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
         tc_fence_after();
         tmem_ld32(t + T_DP + w * 32, s);
         tmem_ld_wait();
-        uint32_t pk[16];
+        if (x.steps == 1 || (TWICE && n < x.first())) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float2 y = add2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), nd);
-          const float2 ds = mul2(pr[k], y);
-          pk[k] = pack2(ds.x, ds.y);
+          for (int k = 0; k < 16; ++k)
+            lacks = fma2(pr[k], add2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), nd), lacks);
+          if (!TWICE || x.steps == 1 || n + 1 == x.first()) {
+            settle();
+            if (!ok) break;
+          }
         }
-        tmem_st16(t + T_DS + w * 16, pk);
-        tmem_st_wait();
+        if (!TWICE || n >= x.first()) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            pr[k] = mul2(pr[k], add2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), nd));
+            pk[k] = pack2(pr[k].x, pr[k].y);
+          }
+          tmem_st16(t + T_DS + w * 16, pk);
+          tmem_st_wait();
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(m.ds_full);
+        if (open) {  // (below the next block's products)
+#pragma unroll
+          for (int k = 0; k < 16; k += 4)
+            lacks = add2(lacks, add2(add2(pr[k], pr[k + 1]), add2(pr[k + 2], pr[k + 3])));
+        }
       }
+      if (ok && open) settle();
       if (ok && x.steps > 0) ok = warp_wait(m.acc_full, accs & 1, m.abort_flag, p.err);
       accs += x.steps > 0;
       base += x.steps;
@@ -737,8 +794,10 @@ template <int NC>
 int launch(const AttnArgs& a, cudaStream_t s) {
   using C = Cfg<NC>;
   const int kv_heads = a.heads / a.group;
-  static std::atomic<uint64_t> dq_done{0}, dkv_done{0};
-  int rc = allow_smem(reinterpret_cast<const void*>(attn_dq_kernel<NC>), C::SMEM, dq_done);
+  static std::atomic<uint64_t> dq_done{0}, dq_twice_done{0}, dkv_done{0};
+  const bool twice = a.window > 1 && a.window <= kFewKeys;
+  const auto dq = twice ? attn_dq_kernel<NC, true> : attn_dq_kernel<NC, false>;
+  int rc = allow_smem(reinterpret_cast<const void*>(dq), C::SMEM, twice ? dq_twice_done : dq_done);
   if (!rc) rc = allow_smem(reinterpret_cast<const void*>(attn_dkv_kernel<NC>), C::SMEM, dkv_done);
   if (rc) return rc;
   CUtensorMap mq, mo, mk, mv;
@@ -751,8 +810,7 @@ int launch(const AttnArgs& a, cudaStream_t s) {
   if ((rc = make_head_map(&mk, a.K, a.hd, kv_heads, std::max<int64_t>(a.Tk, 1), a.ldk, BT))) return rc;
   if ((rc = make_head_map(&mv, a.V, a.hd, kv_heads, std::max<int64_t>(a.Tk, 1), a.ldv, BT))) return rc;
   if (a.Tq > 0 && qb > 0) {
-    attn_dq_kernel<NC><<<dim3(static_cast<unsigned>(lists), static_cast<unsigned>(qb)), C::THREADS,
-                         C::SMEM, s>>>(mq, mo, mk, mv, a);
+    dq<<<dim3(static_cast<unsigned>(lists), static_cast<unsigned>(qb)), C::THREADS, C::SMEM, s>>>(mq, mo, mk, mv, a);
     count_launch();
     if (cudaGetLastError() != cudaSuccess) return QAT_ERR_CUDA;
   }
