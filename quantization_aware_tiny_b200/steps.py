@@ -346,7 +346,8 @@ class HeadMlpStep:
         dZ = dLogits Wemb_q; dWemb = dLogits^T Z; MLP backward -> dX, dWfc, dWproj
     step() takes dLogits from the caller; step_loss() takes the next words and
     trains on their mean cross entropy, without ever holding the logits
-    (logits=False then leaves their buffer out).
+    (logits=False then leaves their buffer out; the loss's workspace, made at its
+    first use, is the size that runs fastest, up to about 1 GiB).
     """
 
     def __init__(self, Wemb, Wfc, Wproj, T, head_bits=8, mlp_bits=6, act="relu2", logits=True):
