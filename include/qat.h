@@ -222,7 +222,8 @@ int qat_mlp_bwd(const float* Wfc, const float* Wproj, const qat_qweight* qfc,
  * another (QAT_ERR_ARG, here and in the calls below).
  * Z holds finite values in every row (a NaN of a row without target would reach
  * dW: its zero gradient is multiplied with the row).  Statistics are fp32, the
- * mean's sum fp64; the same inputs give the same bits.  workspace: qat_workspace_size(QAT_OP_CE_FWD, V, d, T, raw) bytes.
+ * mean's sum fp64; the same inputs give the same bits.
+ * workspace: qat_workspace_size(QAT_OP_CE_FWD, V, d, T, raw) bytes.
  * T = 0 writes mean only.
  * ------------------------------------------------------------------------- */
 int qat_ce_fwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int32_t bits,
@@ -261,9 +262,9 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
  * X, Y [T, heads * head_dim] fp32 or bf16 (dtype), rows ldx / ldy elements
  * apart (multiples of 8; 0 -> heads * head_dim): the heads may be a column
  * range of a wider row, such as the query and key columns of a Q|K|V
- * projection.  Y may be X itself (same stride); otherwise they share
- * no elements (columns of one wider row are fine).  head_dim a multiple of 8; rotary even, at most head_dim and
- * QAT_ROPE_MAX_DIMS.  positions [T] int64, or NULL: row t is at t mod seq_len,
+ * projection.  Y may be X itself (same stride); otherwise they share no elements
+ * (columns of one wider row are fine).  head_dim a multiple of 8; rotary even, at
+ * most head_dim and QAT_ROPE_MAX_DIMS.  positions [T] int64, or NULL: row t is at t mod seq_len,
  * or at t with seq_len = 0.  freqs [rotary / 2] fp64, turns per position: the
  * whole turns are taken off the exact product, so the angle of the given freqs
  * keeps fp32's accuracy at every position to +-2^53 (farther ones are themselves

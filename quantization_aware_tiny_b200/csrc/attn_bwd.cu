@@ -22,13 +22,12 @@
 // gained nothing or lost.
 //
 // P and dS are rounded to bf16 for the second products, as P is in the forward: each
-// off by at most 2^-8 of itself, which leaves dQ, dK and dV 2.5e-3 off in the 2-norm
+// off by at most 2^-8 of itself, which leaves dQ, dK and dV 2.4e-3 off in the 2-norm
 // where their own rounding alone gives 1.7e-3; second halves would be three products
-// more.  delta, lse and all sums are fp32.  They go back to tensor
-// memory and are read from there as operand A.  Both kernels form P as soon as S
-// is there and dS once dP is, so that the products of the next block (and the
-// sums of this one) run below the exponentials; four math warpgroups share a
-// block, 32 of its 128 columns each.
+// more.  delta, lse and all sums are fp32.  P and dS go back to tensor memory and are
+// read from there as operand A.  Both kernels form P as soon as S is there and dS once
+// dP is, so that the products of the next block (and the sums of this one) run below
+// the exponentials; four math warpgroups share a block, 32 of its 128 columns each.
 #include <algorithm>
 #include <atomic>
 
@@ -206,11 +205,12 @@ __device__ __forceinline__ void produce(const Smem<NC>& m, const AttnArgs& p, Wo
 // sum(P * (dP - delta)) is what it lacks.  A row whose keys lie in one block gets it
 // before its dS is formed (all rows of few keys, but for small windows: those tiles are
 // walked twice, the first time for the sum alone); the others take delta as it came,
-// which costs nothing at scores of unit spread (0.0024) and up to 0.0035 at four times
-// that.  dK always gets the mended delta: the sum goes along with dS.  The sums take 3 %
-// of this kernel (150 -> 154 us at 4 x 4,096 tokens of 8 heads of 64); tiles walked twice
-// are a kernel of their own, since the branch around the products that a common one needs
-// took 9 % more.  At windows past 16 keys dQ is 0.0025 off as it is.
+// which costs nothing at scores of unit spread (0.0024), up to 0.0036 at four times that
+// and 0.0065 where every row is nearly one-hot (simulated, 300 to 1,000 keys).  dK always
+// gets the mended delta: the sum goes along with dS.  The sums take 3 % of this kernel
+// (150 -> 154 us at 4 x 4,096 tokens of 8 heads of 64); tiles walked twice are a kernel
+// of their own, since the branch around the products that a common one needs took 9 %
+// more.  At windows past 16 keys dQ is 0.0025 off as it is.
 constexpr int kFewKeys = 16;
 
 // A CTA owns 128 queries of a head.  Tensor memory: S, dP (128 columns each), dS
