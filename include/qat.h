@@ -240,9 +240,11 @@ int qat_ce_fwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
  * target get zero rows of dZ.  The logits are computed again and turned into g
  * a piece of tokens at a time: g exists only for one piece, as bf16 plus the
  * bf16 of what that rounding left (dZ takes the first, and the second at
- * the target; dW takes both, so it is good to about 1e-5).  dZ has the same bits
- * every time (a workspace smaller than asked for may give others); dW's partial sums are added in order where V * d fills the GPU with
- * output tiles, else as they come, as in qat_linear_bwd.  workspace: qat_workspace_size(QAT_OP_CE_BWD, V, d, T, raw)
+ * the target; dW takes both, so it is good to about 1e-5).  Partial sums of both
+ * are added in a fixed order: the same inputs give the same bits every time (a
+ * workspace smaller than asked for may give others, and then a small head's dW is
+ * added as its parts come, as in qat_linear_bwd).
+ * workspace: qat_workspace_size(QAT_OP_CE_BWD, V, d, T, raw)
  * bytes give the pieces that run fastest and also serve qat_ce_fwd; less works
  * with smaller pieces, down to 256 tokens (1024 bytes per word, V rounded up
  * to a multiple of 8, and 1 KiB beside the operand), below which QAT_ERR_WORKSPACE is

@@ -199,18 +199,42 @@ size_t ce_fwd_bytes(int64_t V, int64_t T) {
 size_t ce_bwd_bytes(int64_t V, int64_t rows) {
   return 2 * align_up(rows * ce_ldg(V) * 2) + align_up(rows * 4);
 }
-// Partial products of dZ where a piece has so few tokens that its tiles leave most of
-// the GPU idle and the reduction over the vocabulary is split (0: it is not).  Loss and
-// gradients (dW's two halves in one product and the joins included): one token of 50,000
-// words, d = 512, 361 -> 89 us; 300 of 20,001, d = 256, 165 -> 66 us; 1,500 of 50,257,
-// d = 768, 689 -> 544 us.
-size_t ce_slab_bytes(int64_t V, int64_t d, int64_t n) {
-  const Slabs s = f32_slabs(n, d, V);
-  return n > 0 && s.count > 1 ? align_up(s.count * s.rows * d * 4) : 0;
+// The products of a piece of n tokens without their addresses: dZ = g . Wq, and dW = g^T . Z
+// with both halves of g.
+GemmDesc ce_dz_product(int64_t V, int64_t d, int64_t n) {
+  GemmDesc x;
+  x.M = n; x.N = d; x.K = V;
+  x.b_mn = true;
+  return x;
+}
+GemmDesc ce_dw_product(int64_t V, int64_t d, int64_t n, const void* half) {
+  GemmDesc w;
+  w.M = V; w.N = d; w.K = n;
+  w.A2 = half;
+  w.a_mn = w.b_mn = true;
+  w.epi = EPI_F32;
+  w.k_run = kCeTokenRun;
+  return w;
+}
+// Partial products where the output tiles leave most of the GPU idle and the reduction is
+// split (0: it is not): dZ of a piece of few tokens, over the vocabulary, and dW of a small
+// head, over the tokens; both are joined in order, one after the other in the same place.
+// Loss and gradients with dZ split (dW's two halves in one product and the joins
+// included): one token of 50,000 words, d = 512, 361 -> 89 us; 300 of 20,001, d = 256,
+// 165 -> 66 us; 1,500 of 50,257, d = 768, 689 -> 544 us.
+size_t ce_slab_bytes(const GemmDesc& g) {
+  if (g.M <= 0 || g.K <= 0) return 0;
+  const Slabs s = f32_slabs(g);
+  return s.count > 1 ? align_up(s.count * s.rows * g.N * 4) : 0;
+}
+size_t ce_slab_bytes(int64_t V, int64_t d, int64_t n, bool dz, bool dw) {
+  const int half = 0;
+  return std::max(dz ? ce_slab_bytes(ce_dz_product(V, d, n)) : 0,
+                  dw ? ce_slab_bytes(ce_dw_product(V, d, n, &half)) : 0);
 }
 // What every piece of T tokens, `rows` at a time, can use.
-size_t ce_slab_bytes_max(int64_t V, int64_t d, int64_t T, int64_t rows) {
-  return std::max(ce_slab_bytes(V, d, rows), ce_slab_bytes(V, d, T % rows));
+size_t ce_slab_bytes_max(int64_t V, int64_t d, int64_t T, int64_t rows, bool dz, bool dw) {
+  return std::max(ce_slab_bytes(V, d, rows, dz, dw), ce_slab_bytes(V, d, T % rows, dz, dw));
 }
 
 // ---- attention
@@ -336,7 +360,7 @@ size_t qat_workspace_size(int32_t op, int32_t N_or_d, int32_t K_or_H, int64_t T,
       size_t n = T > 0 ? ce_fwd_bytes(a, T) : 0;
       if (op == QAT_OP_CE_BWD && T > 0) {
         const int64_t rows = ce_rows_wanted(a, b, T);
-        n = std::max(n, ce_bwd_bytes(a, rows) + ce_slab_bytes_max(a, b, T, rows));
+        n = std::max(n, ce_bwd_bytes(a, rows) + ce_slab_bytes_max(a, b, T, rows, true, true));
       }
       return n + (raw_weights ? operand_bytes(a, b) : 0);
     }
@@ -772,7 +796,7 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
   float* rem = static_cast<float*>(ws.take(static_cast<size_t>(rows) * 4));
   if (!ghi || !glo || !rem) return QAT_ERR_WORKSPACE;
   // (a smaller workspace than asked for may leave no room for these: the product is then whole)
-  const size_t slab_bytes = dZ ? ce_slab_bytes_max(V, d, T, rows) : 0;
+  const size_t slab_bytes = ce_slab_bytes_max(V, d, T, rows, dZ != nullptr, dW != nullptr);
   float* slabs = slab_bytes ? static_cast<float*>(ws.take(slab_bytes)) : nullptr;
   // (dW reads the rows of Z after their dZ is written)
   if (outputs_shared({Span(dZ, T * d * 2), Span(dW, static_cast<int64_t>(V) * d * 4),
@@ -802,11 +826,10 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
     rc = launch_gemm(g, stream);
     if (rc) return rc;
     if (dZ) {  // dZ = g . Wq from g's bf16 half, the target's remainder added at the end
-      GemmDesc x;
+      GemmDesc x = ce_dz_product(V, d, n);
       x.A = ghi; x.lda = ldg;
-      x.B = op; x.ldb = d; x.b_mn = true;
-      x.M = n; x.N = d; x.K = V;
-      const Slabs sl = f32_slabs(n, d, V);
+      x.B = op; x.ldb = d;
+      const Slabs sl = f32_slabs(x);
       if (slabs && sl.count > 1) {  // few tokens: over parts of the vocabulary, joined after
         x.epi = EPI_F32;
         x.slabs = true;
@@ -840,15 +863,29 @@ int qat_ce_bwd(const float* W, const qat_qweight* qw, int32_t V, int32_t d, int3
     // 1e-3 off, so its remainder is multiplied too (and first: it is small), in the same
     // pass: dW of a large vocabulary is written once, not written, read and written.
     if (dW) {
-      GemmDesc w;
-      w.A = glo; w.A2 = ghi; w.lda = ldg; w.a_mn = true;
-      w.B = Zp; w.ldb = ldz; w.b_mn = true;
-      w.M = V; w.N = d; w.K = n;
-      w.epi = EPI_F32;
+      GemmDesc w = ce_dw_product(V, d, n, ghi);
+      w.A = glo; w.lda = ldg;
+      w.B = Zp; w.ldb = ldz;
       w.D = dW; w.ldd = d;
-      w.k_run = kCeTokenRun;
-      w.accumulate = accumulate_dW != 0 || t0 > 0;
-      rc = launch_gemm(w, stream);
+      const bool add = accumulate_dW != 0 || t0 > 0;
+      const Slabs sl = f32_slabs(w);
+      if (slabs && sl.count > 1) {  // a small head: over parts of the tokens, joined after
+        w.slabs = true;
+        w.D = slabs;
+        rc = launch_gemm(w, stream);
+        if (rc) return rc;
+        CeDw j{};
+        j.slabs = slabs;
+        j.count = sl.count;
+        j.stride = sl.rows * d;
+        j.dW = dW;
+        j.n = static_cast<int64_t>(V) * d;
+        j.add = add;
+        rc = launch_ce_dw_join(j, stream);
+      } else {
+        w.accumulate = add;
+        rc = launch_gemm(w, stream);
+      }
       if (rc) return rc;
     }
   }

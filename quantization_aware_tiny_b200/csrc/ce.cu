@@ -185,6 +185,25 @@ __global__ void __launch_bounds__(32 * kDzParts) ce_dz_join_kernel(const CeDz j)
   o[1] = __floats2bfloat162_rn(a.z, a.w);
 }
 
+// The slabs of dW, four columns a thread.  Bound by reading count * n floats that the
+// product has just left in L2 (heads whose tiles fill less than half the GPU: under 10 MB a
+// slab, and about as many tiles in all slabs together as CTAs or pairs).
+constexpr int kDwThreads = 256;
+__global__ void __launch_bounds__(kDwThreads) ce_dw_join_kernel(const CeDw j) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kDwThreads + threadIdx.x) * 4;
+  if (i >= j.n) return;
+  float4 a = j.add ? *reinterpret_cast<const float4*>(j.dW + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int s = 0; s < j.count; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(j.slabs + s * j.stride + i);
+    a.x += v.x;
+    a.y += v.y;
+    a.z += v.z;
+    a.w += v.w;
+  }
+  *reinterpret_cast<float4*>(j.dW + i) = a;
+}
+
 int64_t join_blocks(int64_t T) { return T <= kJoinSingle ? T : (T + kJoinRows - 1) / kJoinRows; }
 
 }  // namespace
@@ -199,6 +218,13 @@ int launch_ce_dz_join(const CeDz& j, cudaStream_t stream) {
   if (j.n > (1ll << 31) - 1 || columns > 65535) return QAT_ERR_SHAPE;
   const int parts = std::min(kDzParts, (j.count + 3) / 4);  // four slabs a thread or more
   ce_dz_join_kernel<<<dim3(static_cast<unsigned>(j.n), static_cast<unsigned>(columns)), dim3(32, parts), 0, stream>>>(j);
+  count_launch();
+  return cuda_status(cudaGetLastError());
+}
+
+int launch_ce_dw_join(const CeDw& j, cudaStream_t stream) {
+  const int64_t blocks = (j.n / 4 + kDwThreads - 1) / kDwThreads;
+  ce_dw_join_kernel<<<static_cast<unsigned>(blocks), kDwThreads, 0, stream>>>(j);
   count_launch();
   return cuda_status(cudaGetLastError());
 }

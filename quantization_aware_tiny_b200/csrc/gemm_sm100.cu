@@ -94,9 +94,10 @@ struct Cfg {
 struct KArgs {
   int M, N;
   int num_m_blk, num_n_blk, splits, kblk_total, kblk_per_split, num_tiles;
-  int ordered;  // EPI_F32_ATOMIC: one CTA (pair) takes all splits of a tile, in order
+  int runs;     // EPI_F32_ATOMIC: a CTA (pair) takes this many splits of a tile, in order (0: each by itself)
+  int groups;   // groups of so many splits per tile
   int kblk_a2;    // fp32 outputs of MN-major operands: k-blocks from here on are A2's (tmR), with B from its start
-  int slab_rows;  // EPI_F32: row distance of the splits' outputs (0: one output)
+  int slab_rows;  // fp32 outputs: row distance of the splits' (or their groups') outputs (0: one output)
   void* D;
   int64_t ldd;
   void* D2;
@@ -414,13 +415,18 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
     const int64_t s = q * p.num_tiles / units;
     return s < x + p.num_m_blk ? static_cast<int>(s - x) : 0;
   };
-  // Ordered splits: tile numbers run split-fastest and a CTA (pair) walks all
-  // splits of a tile before its next tile, so every element's partial sums are
-  // added in the same order each time.
-  const bool ordered = EPI == EPI_F32_ATOMIC && p.ordered != 0;
-  if (ordered) t_begin = unit * p.splits;
+  // Ordered splits: tile numbers run split-fastest and a CTA (pair) walks a group of
+  // splits of a tile (all of them, or those of one slab) before its next group, so every
+  // element's partial sums are added in the same order each time.
+  const bool ordered = EPI == EPI_F32_ATOMIC && p.runs != 0;
+  auto group_begin = [&](int g) { return g / p.groups * p.splits + g % p.groups * p.runs; };
+  if (ordered) t_begin = group_begin(unit);
   auto next_tile = [&](int t) {
-    if (ordered) return (t + 1) % p.splits ? t + 1 : t + 1 + (units - 1) * p.splits;
+    if (ordered) {
+      const int sp = t % p.splits;
+      if (sp + 1 < p.splits && (sp + 1) % p.runs) return t + 1;
+      return group_begin(t / p.splits * p.groups + sp / p.runs + units);
+    }
     return t + t_step;
   };
   auto tile_nb = [&](int t) {
@@ -784,9 +790,11 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI, FB>::THREADS, 1)
         if (lane == 0) {
           const uint8_t* s0 = staging + (buf0 - smem_u32(staging));
           if constexpr (EPI == EPI_F32_ATOMIC) {
-            // (the first of ordered splits writes: nothing has to be cleared before)
-            if (ordered && !p.accumulate && tile_sp(tile) == 0) tma_store_2d(&tmD, s0, col0, row0);
-            else tma_reduce_add_2d(&tmD, s0, col0, row0);
+            // (the first of a group of ordered splits writes: nothing has to be cleared before)
+            const int sp = ordered ? tile_sp(tile) : 0;
+            const int row = ordered ? row0 + sp / p.runs * p.slab_rows : row0;
+            if (ordered && !p.accumulate && sp % p.runs == 0) tma_store_2d(&tmD, s0, col0, row);
+            else tma_reduce_add_2d(&tmD, s0, col0, row);
           } else if constexpr (EPI == EPI_F32) {
             tma_store_2d(&tmD, s0, col0, row0 + tile_sp(tile) * p.slab_rows);
           } else if constexpr (epi_act_fwd(EPI)) {
@@ -1045,17 +1053,21 @@ int64_t ce_slots(int64_t M, int64_t N) {
   return (N + BN - 1) / BN * 2;
 }
 
-Slabs f32_slabs(int64_t M, int64_t N, int64_t K) {
+Slabs f32_slabs(const GemmDesc& g) {
   int BN;
   bool pair;
-  choose_tile(M, N, false, false, &BN, &pair);
-  const int64_t tile_m = pair ? 2 * BM : BM, m_blk = (M + tile_m - 1) / tile_m;
-  const int64_t tiles = m_blk * ((N + BN - 1) / BN);
+  choose_tile(g.M, g.N, false, g.a_mn, &BN, &pair);
+  const int64_t tile_m = pair ? 2 * BM : BM, m_blk = (g.M + tile_m - 1) / tile_m;
+  const int64_t tiles = m_blk * ((g.N + BN - 1) / BN);
   const int units = pair ? sm_count() / 2 : sm_count();
-  const int kblk = static_cast<int>((K + BK - 1) / BK);
-  const int s = 2 * tiles >= units ? 1 : choose_splits(static_cast<int>(tiles), kblk, units);
-  const int per = (kblk + s - 1) / s;
-  return Slabs{(kblk + per - 1) / per, m_blk * tile_m};  // no empty split
+  const int kblk = static_cast<int>((g.K + BK - 1) / BK) * (g.A2 ? 2 : 1);
+  int s = 2 * tiles >= units ? 1 : choose_splits(static_cast<int>(tiles), kblk, units);
+  int per = (kblk + s - 1) / s;
+  const int run = static_cast<int>(g.k_run / BK);
+  const int runs = run > 0 ? (per + run - 1) / run : 1;
+  per = (kblk + s * runs - 1) / (s * runs);
+  s = (kblk + per - 1) / per;  // no empty split
+  return Slabs{(s + runs - 1) / runs, m_blk * tile_m, runs, s, per};
 }
 
 bool fused_b_supported(int64_t M, int64_t N, int64_t K, int epi) {
@@ -1089,7 +1101,7 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
       (g.R && (g.ldr & 7)))
     return QAT_ERR_SHAPE;
   if (g.A2 && (!g.a_mn || !g.b_mn || g.epi != EPI_F32 || !aligned16(g.A2))) return QAT_ERR_ARG;
-  if (g.slabs && (g.a_mn || !g.b_mn || g.epi != EPI_F32 || g.accumulate)) return QAT_ERR_ARG;
+  if (g.slabs && (!g.b_mn || g.epi != EPI_F32 || g.accumulate)) return QAT_ERR_ARG;
   if (g.M > (1ll << 31) - 256 || g.N > (1 << 30) || g.K > (1ll << 31) - 256) return QAT_ERR_SHAPE;
 
   int BN;
@@ -1127,12 +1139,17 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
   int epi = g.epi;
   int64_t d_rows = g.M;
   if (g.slabs) {
-    const Slabs sl = f32_slabs(g.M, g.N, g.K);
-    a.splits = sl.count;
-    a.kblk_per_split = (a.kblk_total + sl.count - 1) / sl.count;
+    const Slabs sl = f32_slabs(g);
+    a.splits = sl.splits;
+    a.kblk_per_split = sl.per;
     a.slab_rows = static_cast<int>(sl.rows);
     d_rows = sl.count * sl.rows;
     if (d_rows > (1ll << 31) - 256) return QAT_ERR_SHAPE;
+    if (sl.runs > 1) {  // the parts of a slab are added by one CTA (pair)
+      a.runs = sl.runs;
+      a.groups = sl.count;
+      epi = EPI_F32_ATOMIC;
+    }
   } else if (epi == EPI_F32 || epi == EPI_F32_ATOMIC) {
     const int tiles = a.num_m_blk * a.num_n_blk;
     // Split K only while the output tiles occupy fewer than half the CTAs
@@ -1143,15 +1160,17 @@ int launch_gemm(const GemmDesc& g, cudaStream_t stream) {
     const int cunits = pair ? sm_count() / 2 : sm_count();
     int s = (2 * tiles >= cunits) ? 1 : choose_splits(tiles, a.kblk_total, cunits);
     const int run = static_cast<int>(g.k_run / BK);
-    if (run > 0 && (a.kblk_total + s - 1) / s > run) {
-      a.ordered = s == 1;
-      s = (a.kblk_total + run - 1) / run;
-    }
+    const bool ordered = run > 0 && s == 1 && a.kblk_total > run;
+    if (run > 0 && (a.kblk_total + s - 1) / s > run) s = (a.kblk_total + run - 1) / run;
     a.kblk_per_split = (a.kblk_total + s - 1) / s;
     s = (a.kblk_total + a.kblk_per_split - 1) / a.kblk_per_split;  // no empty split
     a.splits = s;
+    if (ordered) {
+      a.runs = s;
+      a.groups = 1;
+    }
     if (s > 1 || g.accumulate) {
-      if (!g.accumulate && !a.ordered) {
+      if (!g.accumulate && !ordered) {
         cudaError_t e = (g.ldd == g.N)
                             ? cudaMemsetAsync(g.D, 0, static_cast<size_t>(g.M * g.N) * 4, stream)
                             : cudaMemset2DAsync(g.D, static_cast<size_t>(g.ldd) * 4, 0,

@@ -81,8 +81,8 @@ struct GemmDesc {
   // fp32 epilogues of MN-major operands: a second A of the same shape and stride,
   // multiplied with the same B into the same accumulators, D = A^T B + A2^T B.
   const void* A2 = nullptr;
-  // EPI_F32 with a K-major A: the reduction is split as f32_slabs() says and D holds
-  // the partial products, slab s at row s * rows (added up by the caller's next kernel).
+  // EPI_F32: the reduction is split as f32_slabs() says and D holds the partial products,
+  // slab s at row s * rows (added up by the caller's next kernel, in order).
   bool slabs = false;
   // Fused quantizing B producer: when set, B / ldb are ignored and the kernel
   // builds the bf16 operand bf16(fl32(c * s)) of this fp32 weight [N,K]
@@ -98,12 +98,14 @@ struct GemmDesc {
 int64_t ce_slots(int64_t M, int64_t N);
 
 // Slabs that the product of `slabs` writes: count (1: the output's tiles alone occupy
-// half the CTAs or pairs, a split would not pay) and rows of each.
+// half the CTAs or pairs, a split would not pay) and rows of each.  A slab is the sum of
+// up to `runs` of the `splits` parts of the reduction, `per` k-blocks each.
 struct Slabs {
   int count;
   int64_t rows;
+  int runs, splits, per;
 };
-Slabs f32_slabs(int64_t M, int64_t N, int64_t K);
+Slabs f32_slabs(const GemmDesc& g);
 
 // Whether launch_gemm can quantize B inside the GEMM for this shape / epilogue.
 bool fused_b_supported(int64_t M, int64_t N, int64_t K, int epi);

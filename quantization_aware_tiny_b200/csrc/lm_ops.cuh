@@ -38,6 +38,17 @@ struct CeDz {
 };
 int launch_ce_dz_join(const CeDz& j, cudaStream_t stream);
 
+// ---- cross entropy, small heads: dW (+)= the sum of the product's slabs, in order
+struct CeDw {
+  const float* slabs;  // [count][stride]
+  int count;
+  int64_t stride;
+  float* dW;  // [n], n a multiple of 4
+  int64_t n;
+  bool add;
+};
+int launch_ce_dw_join(const CeDw& j, cudaStream_t stream);
+
 // ---- rotary positions (row strides in elements; Y may equal X)
 struct RopeArgs {
   const void* X;

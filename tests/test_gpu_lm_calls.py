@@ -133,3 +133,35 @@ def test_rope_far_positions_against_exact_products(interleaved):
     tol += 2.0 ** -24 * want.abs()
     err = (f64(y).reshape(want.shape) - want).abs()
     assert bool((err <= tol).all()), float((err - tol).max())
+
+
+@pytest.mark.parametrize("shape", [(130, 1024, 512), (1000, 40, 8), (5000, 1000, 256), (9000, 520, 72), (20000, 2001, 512),
+                                   (12000, 4000, 512), (300, 257, 640)])
+def test_ce_gradients_of_small_heads_have_the_same_bits(shape):
+    """Heads whose output tiles leave most of the GPU idle: the tokens are split, and their
+    parts added in one order, run after run, added to a gradient, and from raw words."""
+    from test_gpu_cross_entropy import check, make, run, workspace
+    T, V, d = shape
+    c = make(T, V, d, seed=T, ignored=0.1)
+    first = run(c, V, d)
+    if T * V <= 6_000_000:
+        check(c, V, d, first)
+    base = torch.randn(V, d, device="cuda")
+    sums = []
+    for _ in range(6):
+        got = run(c, V, d)
+        assert torch.equal(got[3], first[3]) and torch.equal(got[4], first[4])
+        acc = base.clone()
+        qat.qat_ce_bwd(c["Zd"], c["td"], first[1], 8, qw=c["q"], gscale=first[2][1:], dW=acc, accumulate_dW=True,
+                       workspace=workspace(qat.QAT_OP_CE_BWD, V, d, T))
+        sums.append(acc)
+    raw = torch.empty_like(base)
+    qat.qat_ce_bwd(c["Zd"], c["td"], first[1], 8, W=c["W"].cuda(), gscale=first[2][1:], dW=raw,
+                   workspace=workspace(qat.QAT_OP_CE_BWD, V, d, T, True))
+    torch.cuda.synchronize()
+    assert qat.device_error() == 0
+    assert all(torch.equal(a, sums[0]) for a in sums) and torch.equal(raw, first[4])
+    # base added first: 64 slabs at most in a piece, a half step of the running sum each
+    pieces = -(-T // 256)
+    allowed = 2.0 ** -24 * (64 * pieces + 1) * (base.abs().max() + 64 * first[4].abs().max())
+    assert float((sums[0] - base - first[4]).abs().max()) <= float(allowed)
